@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["moe_api.hip", "route.hip", "dispatch.hip", "ffn.hip", "ffn_decode.hip", "ffn_prefill.hip",
-           "ffn_prefill_f8.hip", "combine.hip", "pack.cpp"]
+           "ffn_prefill_f8.hip", "combine.hip", "pack.cpp", "fp8_linear.hip", "norm_rope.hip", "attention.hip"]
 ARCH = "gfx950"
 
 

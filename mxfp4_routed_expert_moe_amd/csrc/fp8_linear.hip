@@ -1,0 +1,425 @@
+// Matrix product in E4M3 with one scale per block of 128
+// (include/moe_attention.h, moe_fp8_linear): y = x W^T, W as stored with a scale
+// per 128 x 128 block, x quantised here with a scale per token and 128 columns.
+//
+// One v_mfma_scale_f32_16x16x128_f8f6f4 covers exactly one block of K, so a
+// scale is constant inside it.  E8M0 scales go to the instruction, which applies
+// them for nothing: the whole K is summed in one accumulator.  float32 scales
+// cannot: each block's product starts from zero and is added as
+// acc += (sx * sw) * product, four vector FMAs per MFMA, which run beside the
+// matrix cores.  The weights are the A operand (result rows) and the tokens
+// the B operand (result columns), so a lane's four results are four
+// consecutive outputs of one token, and its token's scale is a lane's scalar.
+//
+// Past the end of K the quantised x is zero (its rows are padded to whole
+// blocks), and W repeats its row's last 16 bytes: zero times a weight the row holds
+// anyway.  Past the end of N and T the last row is repeated and not stored.
+#include <algorithm>
+
+#include "../../include/moe_attention.h"
+#include "lds_dma.h"
+#include "moe_internal.h"
+
+namespace moe {
+
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr float kFp8Max = 448.f;
+constexpr float kFloor = 0x1p-100f;  // least block maximum: keeps every scale and its inverse normal
+
+// ---------------------------------------------------------------- quantisation
+// The scale of a block from its largest magnitude, as the word the kernels
+// take (the E8M0 byte, or the float32's bits), and the factor that x is
+// multiplied by.
+template <bool F32>
+__device__ __forceinline__ uint32_t block_scale(float amax, float& inv) {
+  amax = fmaxf(amax, kFloor);
+  if (F32) {
+    inv = kFp8Max / amax;
+    return __float_as_uint(amax / kFp8Max);
+  }
+  // amax = 1.m * 2^(E - 127) and 448 = 1.75 * 2^8: the least e with amax <= 448 * 2^(e - 127)
+  const uint32_t b = __float_as_uint(amax);
+  const uint32_t e = (b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  inv = __uint_as_float((254 - e) << 23);
+  return e;
+}
+
+__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Four consecutive values (two words of bf16 pairs) to four codes.
+__device__ __forceinline__ uint32_t codes4(uint32_t w0, uint32_t w1, float inv) {
+  int c = __builtin_amdgcn_cvt_pk_fp8_f32(lo_bf16(w0) * inv, hi_bf16(w0) * inv, 0, false);
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(lo_bf16(w1) * inv, hi_bf16(w1) * inv, c, true));
+}
+
+__device__ __forceinline__ float max_abs(u32x4 w, float m) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(lo_bf16(w[i])), fabsf(hi_bf16(w[i]))));
+  return m;
+}
+
+// codes [T, Kp] (Kp = K padded to whole blocks, zeros there), scales [Kp / 128, T].
+// 16 lanes per block, 8 values each.
+template <bool F32>
+__global__ __launch_bounds__(256) void fp8_quant_kernel(const uint16_t* __restrict__ x, int64_t x_stride, int T, int K,
+                                                        int kb, uint8_t* __restrict__ codes,
+                                                        uint32_t* __restrict__ scales) {
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  if (u >= static_cast<int64_t>(T) * kb) return;
+  const int64_t t = u / kb;
+  const int b = static_cast<int>(u - t * kb), k = 128 * b + 8 * (threadIdx.x & 15);
+  u32x4 w = {0, 0, 0, 0};
+  if (k < K) w = ld16(x + t * x_stride + k);
+  float m = max_abs(w, 0.f);
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 16));
+  float inv;
+  const uint32_t s = block_scale<F32>(m, inv);
+  const u32x2 c = {codes4(w[0], w[1], inv), codes4(w[2], w[3], inv)};
+  *reinterpret_cast<u32x2*>(codes + t * (128 * kb) + k) = c;
+  if ((threadIdx.x & 15) == 0) scales[static_cast<int64_t>(b) * T + t] = s;
+}
+
+// ---------------------------------------------------------------- the product of one block
+__device__ __forceinline__ i32x8 join(u32x4 a, u32x4 b) {
+  return i32x8{static_cast<int>(a[0]), static_cast<int>(a[1]), static_cast<int>(a[2]), static_cast<int>(a[3]),
+               static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3])};
+}
+
+// acc += the scaled product of one 128-column block.  sw is W's scale word (the
+// same in all lanes), sx the lane's token's; f32: their product, taken once per
+// token tile.
+template <bool F32>
+__device__ __forceinline__ void block_mfma(i32x8 w, i32x8 x, f32x4& acc, int sw, int sx, float f32) {
+  if (F32) {
+    const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+    // scale operands of 127: 1.0
+    const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, z, 0, 0, 0, 127, 0, 127);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(f32, p[i], acc[i]);
+  } else {
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, 0, 0, 0, sw, 0, sx);
+  }
+}
+
+// W's scale of (128-row block nb, column block b), as a word.
+template <bool F32>
+__device__ __forceinline__ uint32_t weight_scale(const void* s, int64_t i) {
+  return F32 ? static_cast<const uint32_t*>(s)[i] : static_cast<const uint8_t*>(s)[i];
+}
+
+// Four consecutive outputs n .. n + 3 of token t.
+__device__ __forceinline__ void store4(uint16_t* y, int64_t y_stride, int64_t t, int n, int N, bool wide, f32x4 v) {
+  uint16_t* p = y + t * y_stride + n;
+  if (wide && n + 4 <= N) {
+    const u32x2 w = {float_to_bf16_bits(v[0]) | static_cast<uint32_t>(float_to_bf16_bits(v[1])) << 16,
+                     float_to_bf16_bits(v[2]) | static_cast<uint32_t>(float_to_bf16_bits(v[3])) << 16};
+    *reinterpret_cast<u32x2*>(p) = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < N) p[i] = float_to_bf16_bits(v[i]);
+  }
+}
+
+struct LinearArgs {
+  const uint16_t* x;
+  int64_t x_stride, y_stride;
+  const uint8_t* w;
+  const void* w_scale;
+  uint16_t* y;
+  const uint8_t* codes;    // quantised x [T, 128 kb]
+  const uint32_t* scales;  // [kb, T]
+  int T, N, K, kb;         // kb: blocks of K
+  int n_tiles, t_tiles;
+  bool wide;               // rows of y take 8-byte stores
+};
+
+// ---------------------------------------------------------------- few tokens
+// A block holds 16 rows of W and 16 * MT tokens; its NW waves take the blocks of
+// K in turn, straight from memory, and meet in LDS.  W is read once per token
+// block: the kernel streams it.  QUANT: x is quantised on the way in (each of
+// the four lanes of a token holds 32 columns of the block).
+constexpr int kNW = 8;
+
+template <int MT, bool F32, bool QUANT>
+__global__ __launch_bounds__(64 * kNW) void fp8_few_kernel(LinearArgs a) {
+  constexpr int kU = MT == 1 ? 4 : 2;  // blocks of K in flight per wave
+  __shared__ f32x4 part[kNW][MT][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int r = lane & 15, g = lane >> 4;
+  const int n0 = 16 * blockIdx.x, t0 = 16 * MT * blockIdx.y;
+  const uint8_t* wp = a.w + static_cast<int64_t>(min(n0 + r, a.N - 1)) * a.K;
+  const int64_t srow = static_cast<int64_t>(n0 >> 7) * a.kb;
+  const int last = a.K - 16;
+
+  f32x4 acc[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  for (int b0 = wave; b0 < a.kb; b0 += kNW * kU) {
+    u32x4 wv[kU][2], xv[kU][MT][QUANT ? 4 : 2];
+    uint32_t sw[kU], sx[kU][MT];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int b = min(b0 + u * kNW, a.kb - 1);
+      const int k = 128 * b + 32 * g;
+      wv[u][0] = ld16(wp + min(k, last));
+      wv[u][1] = ld16(wp + min(k + 16, last));
+      sw[u] = weight_scale<F32>(a.w_scale, srow + b);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int t = min(t0 + 16 * m + r, a.T - 1);
+        if (QUANT) {
+          const uint16_t* p = a.x + t * a.x_stride + k;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            xv[u][m][i] = u32x4{0, 0, 0, 0};
+            if (k + 8 * i < a.K && t0 + 16 * m + r < a.T) xv[u][m][i] = ld16(p + 8 * i);
+          }
+        } else {
+          const uint8_t* p = a.codes + static_cast<int64_t>(t) * (128 * a.kb) + k;
+          xv[u][m][0] = ld16(p);
+          xv[u][m][1] = ld16(p + 16);
+          sx[u][m] = a.scales[static_cast<int64_t>(b) * a.T + t];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (b0 + u * kNW >= a.kb) break;
+      const i32x8 wf = join(wv[u][0], wv[u][1]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        i32x8 xf;
+        if (QUANT) {
+          float top = 0.f, inv;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = max_abs(xv[u][m][i], top);
+          top = fmaxf(top, __shfl_xor(top, 16, 64));
+          top = fmaxf(top, __shfl_xor(top, 32, 64));
+          sx[u][m] = block_scale<F32>(top, inv);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            xf[2 * i] = static_cast<int>(codes4(xv[u][m][i][0], xv[u][m][i][1], inv));
+            xf[2 * i + 1] = static_cast<int>(codes4(xv[u][m][i][2], xv[u][m][i][3], inv));
+          }
+        } else {
+          xf = join(xv[u][m][0], xv[u][m][1]);
+        }
+        const float f = F32 ? __uint_as_float(sw[u]) * __uint_as_float(sx[u][m]) : 0.f;
+        block_mfma<F32>(wf, xf, acc[m], static_cast<int>(sw[u]), static_cast<int>(sx[u][m]), f);
+      }
+    }
+  }
+
+#pragma unroll
+  for (int m = 0; m < MT; ++m) part[wave][m][lane] = acc[m];
+  __syncthreads();
+  if (wave >= MT) return;
+  f32x4 v = part[0][wave][lane];
+#pragma unroll
+  for (int i = 1; i < kNW; ++i) v += part[i][wave][lane];
+  const int t = t0 + 16 * wave + r;
+  if (t < a.T) store4(a.y, a.y_stride, t, n0 + 4 * g, a.N, a.wide, v);
+}
+
+// ---------------------------------------------------------------- many tokens
+// A block holds BN rows of W and BT tokens, its waves WN x WT parts of that.  Both
+// operands come through LDS by DMA in two stages of one block of K: 16-byte
+// chunk c of a 128-byte row r sits at slot c ^ ((r / 2) mod 8), which spreads the 16
+// rows of a fragment read over all banks.  The two stages are variables of
+// their own, so that the compiler does not wait for the DMA into one before
+// it reads the other.
+__device__ __forceinline__ int slot(int r, int c) { return c ^ ((r >> 1) & 7); }
+
+template <int BN, int BT, int WN, int WT, bool F32>
+__global__ __launch_bounds__(64 * WN * WT, 2) void fp8_tile_kernel(LinearArgs a) {
+  constexpr int kWaves = WN * WT;
+  constexpr int kN = BN / WN / 16, kT = BT / WT / 16;  // 16 x 16 tiles of a wave
+  constexpr int kWOps = BN / 8 / kWaves, kXOps = BT / 8 / kWaves;  // DMA instructions, 8 rows each
+  static_assert(BN / WN <= 128, "a wave's rows of W lie in one scale block");
+  struct Stage {
+    uint8_t w[BN * 128], x[BT * 128];
+    uint32_t s[BT];
+  };
+  __shared__ __attribute__((aligned(1024))) Stage s0;
+  __shared__ __attribute__((aligned(1024))) Stage s1;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int r = lane & 15, g = lane >> 4;
+
+  // Blocks are dealt to the 8 XCDs in turn: each XCD gets a run of consecutive
+  // units, and a run covers eight token tiles before it goes to the next rows
+  // of W, so that the blocks an XCD runs at once share both operands in its L2.
+  const int total = a.n_tiles * a.t_tiles, per = (total + 7) >> 3;
+  const int unit = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= per || unit >= total) return;
+  const int band = unit / (8 * a.n_tiles), in_band = unit - band * 8 * a.n_tiles;
+  const int wide = min(8, a.t_tiles - 8 * band);
+  const int t0 = (8 * band + in_band % wide) * BT, n0 = (in_band / wide) * BN;
+  const int wn = wave % WN, wt = wave / WN;
+
+  const int Kp = 128 * a.kb;
+  int64_t woff[kWOps], xoff[kXOps];
+  int wk[kWOps];
+#pragma unroll
+  for (int i = 0; i < kWOps; ++i) {
+    const int row = 8 * (kWaves * i + wave) + (lane >> 3);
+    woff[i] = static_cast<int64_t>(min(n0 + row, a.N - 1)) * a.K;
+    wk[i] = 16 * slot(row, lane & 7);
+  }
+#pragma unroll
+  for (int i = 0; i < kXOps; ++i) {
+    const int row = 8 * (kWaves * i + wave) + (lane >> 3);
+    xoff[i] = static_cast<int64_t>(min(t0 + row, a.T - 1)) * Kp + 16 * slot(row, lane & 7);
+  }
+  const int srow = min(t0 + 64 * wave + lane, a.T - 1);
+  auto issue = [&](Stage& to, int b) {
+#pragma unroll
+    for (int i = 0; i < kWOps; ++i)
+      dma16(a.w + woff[i] + min(128 * b + wk[i], a.K - 16), &to.w[1024 * (kWaves * i + wave)]);
+#pragma unroll
+    for (int i = 0; i < kXOps; ++i)
+      dma16(a.codes + xoff[i] + 128 * b, &to.x[1024 * (kWaves * i + wave)]);
+    if (wave < BT / 64) dma4(a.scales + static_cast<int64_t>(b) * a.T + srow, &to.s[64 * wave]);
+  };
+
+  const int64_t wrow = static_cast<int64_t>(min(n0 + wn * (BN / WN), a.N - 1) >> 7) * a.kb;
+  f32x4 acc[kN][kT];
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+#pragma unroll
+    for (int j = 0; j < kT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  uint32_t sw_next = weight_scale<F32>(a.w_scale, wrow);
+  auto step = [&](const Stage& now, Stage& next, int b) {
+    wait_vmcnt<0>();
+    stage_barrier();
+    const uint32_t sw = sw_next;
+    if (b + 1 < a.kb) {
+      issue(next, b + 1);
+      sw_next = weight_scale<F32>(a.w_scale, wrow + b + 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    i32x8 xf[kT];
+    uint32_t sx[kT];
+    float f[kT];
+#pragma unroll
+    for (int j = 0; j < kT; ++j) {
+      const int row = (BT / WT) * wt + 16 * j + r;
+      xf[j] = join(ld16(&now.x[128 * row + 16 * slot(row, g)]), ld16(&now.x[128 * row + 16 * slot(row, 4 + g)]));
+      sx[j] = now.s[row];
+      f[j] = F32 ? __uint_as_float(sx[j]) * __uint_as_float(sw) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int row = (BN / WN) * wn + 16 * i + r;
+      const i32x8 wf = join(ld16(&now.w[128 * row + 16 * slot(row, g)]), ld16(&now.w[128 * row + 16 * slot(row, 4 + g)]));
+#pragma unroll
+      for (int j = 0; j < kT; ++j)
+        block_mfma<F32>(wf, xf[j], acc[i][j], static_cast<int>(sw), static_cast<int>(sx[j]), f[j]);
+    }
+  };
+  issue(s0, 0);
+  for (int b = 0; b < a.kb; b += 2) {
+    step(s0, s1, b);
+    if (b + 1 < a.kb) step(s1, s0, b + 1);
+  }
+
+#pragma unroll
+  for (int j = 0; j < kT; ++j) {
+    const int t = t0 + (BT / WT) * wt + 16 * j + r;
+    if (t >= a.T) continue;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int n = n0 + (BN / WN) * wn + 16 * i + 4 * g;
+      store4(a.y, a.y_stride, t, n, a.N, a.wide, acc[i][j]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline size_t align256(size_t v) { return (v + 255) & ~size_t{255}; }
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+constexpr int kFusedTokens = 16;  // x is quantised inside the few-token kernel up to here
+
+bool shape_ok(int32_t T, int32_t N, int32_t K) {
+  return T >= 0 && T <= MOE_MAX_TOKENS && N > 0 && N <= MOE_MAX_DIM && K > 0 && K <= MOE_MAX_DIM && K % 16 == 0;
+}
+
+template <bool F32>
+void launch(LinearArgs& a, hipStream_t s) {
+  if (a.T <= kFusedTokens) {
+    fp8_few_kernel<1, F32, true><<<dim3(ceil_div(a.N, 16), 1), 64 * kNW, 0, s>>>(a);
+    return;
+  }
+  fp8_quant_kernel<F32><<<static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.T) * a.kb, 16)), 256, 0, s>>>(
+      a.x, a.x_stride, a.T, a.K, a.kb, const_cast<uint8_t*>(a.codes), const_cast<uint32_t*>(a.scales));
+  if (a.T <= 64 || ceil_div(a.N, 128) * ceil_div(a.T, 128) < 128) {
+    if (a.T <= 32)
+      fp8_few_kernel<2, F32, false><<<dim3(ceil_div(a.N, 16), ceil_div(a.T, 32)), 64 * kNW, 0, s>>>(a);
+    else
+      fp8_few_kernel<4, F32, false><<<dim3(ceil_div(a.N, 16), ceil_div(a.T, 64)), 64 * kNW, 0, s>>>(a);
+    return;
+  }
+  auto tiles = [&](int bn, int bt) {
+    a.n_tiles = static_cast<int>(ceil_div(a.N, bn));
+    a.t_tiles = static_cast<int>(ceil_div(a.T, bt));
+    return static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.n_tiles) * a.t_tiles, 8) * 8);
+  };
+  if (ceil_div(a.N, 256) * ceil_div(a.T, 256) >= 256) {
+    const unsigned grid = tiles(256, 256);
+    fp8_tile_kernel<256, 256, 2, 4, F32><<<grid, 512, 0, s>>>(a);
+  } else {
+    const unsigned grid = tiles(128, 128);
+    fp8_tile_kernel<128, 128, 2, 2, F32><<<grid, 256, 0, s>>>(a);
+  }
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+size_t moe_fp8_linear_workspace_size(int32_t T, int32_t N, int32_t K) {
+  if (!moe::shape_ok(T, N, K) || T <= 0) return 0;
+  const size_t kb = moe::ceil_div(K, 128);
+  return moe::align256(static_cast<size_t>(T) * kb * 128) + moe::align256(static_cast<size_t>(T) * kb * 4);
+}
+
+int moe_fp8_linear(const uint16_t* x, int64_t x_stride, int32_t T, int32_t K, const uint8_t* w, const void* w_scale,
+                   int32_t scale_type, int32_t N, uint16_t* y, int64_t y_stride, void* ws, size_t ws_bytes,
+                   void* stream) {
+  if (T < 0) return MOE_EINVAL;
+  if (!moe::shape_ok(T, N, K)) return MOE_ESHAPE;
+  if (scale_type != MOE_SCALE_E8M0 && scale_type != MOE_SCALE_F32) return MOE_EINVAL;
+  if (T == 0) return MOE_OK;
+  if (!x || !w || !w_scale || !y || !ws) return MOE_EINVAL;
+  if (x_stride < K || y_stride < N) return MOE_EINVAL;
+  if (!moe::aligned(x, 16) || x_stride % 8 != 0 || !moe::aligned(w, 16) || !moe::aligned(y, 2) ||
+      !moe::aligned(ws, 256) || (scale_type == MOE_SCALE_F32 && !moe::aligned(w_scale, 4)))
+    return MOE_EALIGN;
+  if (ws_bytes < moe_fp8_linear_workspace_size(T, N, K)) return MOE_EWORKSPACE;
+  moe::LinearArgs a;
+  a.x = x, a.x_stride = x_stride, a.y = y, a.y_stride = y_stride;
+  a.w = w, a.w_scale = w_scale;
+  a.T = T, a.N = N, a.K = K, a.kb = static_cast<int>(moe::ceil_div(K, 128));
+  a.codes = static_cast<const uint8_t*>(ws);
+  a.scales = reinterpret_cast<const uint32_t*>(a.codes + moe::align256(static_cast<size_t>(T) * a.kb * 128));
+  a.n_tiles = a.t_tiles = 0;
+  a.wide = y_stride % 4 == 0 && moe::aligned(y, 8);
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (scale_type == MOE_SCALE_F32)
+    moe::launch<true>(a, s);
+  else
+    moe::launch<false>(a, s);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,542 @@
+"""The attention-side operators on the GPU against float64 references, at the
+sizes, masks, strides and values where they can go wrong.
+
+Bounds.  bf16 has 8 significant bits: rounding to nearest is off by at most u = 2^-8 relative.
+ fp8_linear: the codes are those of the reference exactly, so an output is off by
+  its own rounding, u |y|; by the matrix cores' alignment (each of eight
+  neighbouring products loses what lies below 2^-13 of the largest one's power
+  of two): 8 2^-13 times the sum over the groups of eight of their largest
+  products; and by the float32 sums: at most K + blocks + 2 of them, each off by
+  at most 2^-23 of the sum of magnitudes S.
+ qk_norm_rope: u |y| plus a relative 2^-18 of the magnitudes summed (D / 8 +
+  log2 D + 12 float32 operations of 2^-24 each, at most 2^-17.2 for D = 512: 2^-17 taken).
+ attention: with A = sum p |v|: u |o| for the result, 2 u A for the weights rounded to
+  bf16 (once in the product, once in their sum), and the float32 part: the scores are
+  off by d = (D + 4) 2^-23 (scale max |q| |k|), which changes a weight by a factor e^(+-d) and so
+  the result by at most 2 (e^d - 1) A, and the sums over Lk keys by (Lk + 64) 2^-23 A.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from mxfp4_routed_expert_moe_amd import attention as A  # noqa: E402
+from tests import attention_reference as R  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -8
+BF = torch.bfloat16
+
+
+def _say(*a):
+    print("[attention]", *a, flush=True)
+
+
+def _gpu(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _bf16(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(BF).cuda()
+
+
+def _np(t):
+    return t.detach().float().cpu().double().numpy()
+
+
+# ---------------------------------------------------------------- fp8 linear
+def _weights(g, N, K, kind):
+    codes = g.integers(0, 256, (N, K)).astype(np.uint8)
+    codes[codes & 127 == 127] = 0x30  # no NaN codes
+    nb, kb = -(-N // 128), -(-K // 128)
+    if kind == "e8m0":
+        e = g.integers(114, 121, (nb, kb)).astype(np.uint8)
+        return codes, e, 2.0 ** (e.astype(np.float64) - 127)
+    s = np.float32(g.uniform(1e-4, 1e-2, (nb, kb)))
+    return codes, s, s.astype(np.float64)
+
+
+def _check_linear(y, ref, mag, top, K):
+    tol = U * np.abs(ref) + 2.0 ** -10 * top + (K + -(-K // 128) + 2) * 2.0 ** -23 * mag + 1e-38
+    err = np.abs(_np(y) - ref)
+    assert np.all(err <= tol), f"worst {np.nanmax(err / tol):.3f} of its bound"
+    # rounding alone leaves a relative error of at most u in the 2-norm; the sums add little
+    assert np.linalg.norm(_np(y) - ref) <= 1.1 * U * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("kind", ["e8m0", "float32"])
+@pytest.mark.parametrize("T,N,K", [
+    (1, 1, 16), (1, 6144, 4096), (2, 130, 144), (3, 16, 128), (15, 257, 400), (16, 512, 1040), (17, 100, 256),
+    (31, 129, 2048), (33, 48, 272), (64, 4096, 512), (65, 300, 384), (200, 17, 128), (257, 2000, 528),
+    (700, 3000, 256), (1500, 1537, 656), (4099, 4100, 144)])
+def test_fp8_linear(T, N, K, kind):
+    _say("fp8_linear", T, N, K, kind)
+    g = np.random.default_rng(T * 7919 + N * 31 + K)
+    x = R.bf16(g.normal(0, 1, (T, K)) * np.exp(g.normal(0, 1, K)))
+    codes, s, sv = _weights(g, N, K, kind)
+    y = A.fp8_linear(_bf16(x), _gpu(codes), _gpu(s))
+    rows = np.arange(T) if T * N * K < 3e8 else np.unique(np.r_[0, T - 1, g.integers(0, T, 60)])
+    ref, mag, top = R.fp8_linear(x[rows], codes, sv, kind)
+    _check_linear(y[torch.from_numpy(rows).cuda()], ref, mag, top, K)
+
+
+@pytest.mark.parametrize("kind", ["e8m0", "float32"])
+@pytest.mark.parametrize("T", [5, 40, 600])
+def test_fp8_linear_strides_and_edges(T, kind):
+    """Rows of x and y inside wider buffers, y on an odd element, nothing written beside it; the E8M0 type of torch."""
+    _say("fp8_linear strides", T, kind)
+    g = np.random.default_rng(T)
+    N, K = 333, 272
+    x = R.bf16(g.normal(0, 1, (T, K)))
+    codes, s, sv = _weights(g, N, K, kind)
+    xb = torch.full((T, K + 24), float("nan"), dtype=BF, device="cuda")
+    xb[:, 8:8 + K] = _bf16(x)
+    ref, mag, top = R.fp8_linear(x, codes, sv, kind)
+    sg = _gpu(s) if kind == "float32" else _gpu(s).view(torch.float8_e8m0fnu)
+    for lead, pad in ((3, 5), (8, 3)):
+        yb = torch.full((T, lead + N + pad), 7.0, dtype=BF, device="cuda")
+        A.fp8_linear(xb[:, 8:8 + K], _gpu(codes).view(torch.float8_e4m3fn), sg, y=yb[:, lead:lead + N])
+        _check_linear(yb[:, lead:lead + N], ref, mag, top, K)
+        assert torch.all(yb[:, :lead] == 7) and torch.all(yb[:, lead + N:] == 7)
+
+
+@pytest.mark.parametrize("kind", ["e8m0", "float32"])
+@pytest.mark.parametrize("T", [7, 50, 400])
+def test_fp8_linear_values(T, kind):
+    """Zero, tiny, huge, infinite and NaN tokens among ordinary ones; a NaN weight code."""
+    _say("fp8_linear values", T, kind)
+    g = np.random.default_rng(9)
+    N, K = 160, 400
+    x = R.bf16(g.normal(0, 1, (T, K)))
+    x[0] = 0
+    x[1] = R.bf16(x[1] * 1e-38)
+    x[2] = R.bf16(x[2] * 1e30)
+    x[3, 5], x[4, 399], x[5] = np.inf, np.nan, np.nan
+    codes, s, sv = _weights(g, N, K, kind)
+    sv, s = sv * 2.0 ** -20, (s - 20).astype(np.uint8) if kind == "e8m0" else np.float32(s * 2.0 ** -20)
+    codes[7, 399] = 0x7f
+    y = _np(A.fp8_linear(_bf16(x), _gpu(codes), _gpu(s)))
+    ref, mag, top = R.fp8_linear(x, codes, sv, kind)
+    ref[:, 7] = np.nan
+    assert np.array_equal(np.isnan(y), np.isnan(ref))
+    assert np.isnan(ref[3:6]).all() and not np.isnan(np.delete(ref[6:], 7, 1)).any()
+    ok = ~np.isnan(ref)
+    tol = U * np.abs(ref) + 2.0 ** -10 * top + (K + 6) * 2.0 ** -23 * mag + 1e-38
+    assert np.all(np.abs(y - ref)[ok] <= tol[ok])
+    assert np.all(np.delete(y[0], 7) == 0)
+
+
+def test_fp8_linear_beyond_32_bits():
+    """x and its codes past 2^31 elements."""
+    T, N, K = 140000, 40, 16384
+    _say("fp8_linear", T, N, K)
+    g = np.random.default_rng(1)
+    x = torch.randn(T, K, device="cuda", dtype=BF)
+    codes, s, sv = _weights(g, N, K, "e8m0")
+    y = A.fp8_linear(x, _gpu(codes), _gpu(s))
+    rows = np.r_[0, 1, 65535, 131071, 131072, 131073, T - 2, T - 1]
+    ref, mag, top = R.fp8_linear(_np(x[torch.from_numpy(rows).cuda()]), codes, sv, "e8m0")
+    _check_linear(y[torch.from_numpy(rows).cuda()], ref, mag, top, K)
+
+
+# ---------------------------------------------------------------- norm and rotation
+def _table(P, Rd, base=10000.0):
+    ang = np.arange(P)[:, None] * base ** (-np.arange(0, Rd, 2) / Rd)
+    return np.float32(np.concatenate([np.cos(ang), np.sin(ang)], 1))
+
+
+def _check_rope(out, x, w, pos, cs, off, inter, eps):
+    ref, mag = R.norm_rope(x, w, pos, cs, off, inter, eps)
+    y = _np(out)
+    assert np.array_equal(np.isnan(y), np.isnan(ref))
+    ok = ~np.isnan(ref)
+    assert np.all(np.abs(y - ref)[ok] <= (U * np.abs(ref) + 2.0 ** -17 * mag)[ok])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,Hq,Hk,D,Rd,off", [
+    (1, 1, 0, 8, 0, 0), (1, 32, 8, 128, 128, 0), (3, 4, 4, 64, 64, 0), (5, 5, 1, 64, 32, 32), (2, 64, 1, 512, 64, 448),
+    (7, 3, 2, 72, 48, 24), (4, 40, 8, 192, 64, 128), (9, 8, 2, 256, 256, 0), (2, 9, 1, 328, 16, 8), (600, 6, 2, 128, 96, 8),
+    (400, 128, 2, 64, 64, 0), (130, 70, 6, 256, 128, 64)])
+def test_qk_norm_rope(T, Hq, Hk, D, Rd, off, interleaved):
+    _say("qk_norm_rope", T, Hq, Hk, D, Rd, off, interleaved)
+    g = np.random.default_rng(T + 13 * D + Rd)
+    P = 50
+    q, k = R.bf16(g.normal(0, 3, (T, Hq, D))), R.bf16(g.normal(0, 0.1, (T, Hk, D)))
+    qw, kw = np.float32(g.normal(1, 0.2, D)), np.float32(g.normal(1, 0.2, D))
+    pos = g.integers(0, P, T).astype(np.int32)
+    cs = _table(P, Rd) if Rd else None
+    qo, ko = A.qk_norm_rope(_bf16(q), _bf16(k) if Hk else None, _gpu(qw), _gpu(kw), _gpu(pos), None if cs is None else _gpu(cs),
+                            rot_offset=off, interleaved=interleaved)
+    _check_rope(qo, q, qw, pos, cs, off, interleaved, 1e-6)
+    if Hk:
+        _check_rope(ko, k, kw, pos, cs, off, interleaved, 1e-6)
+
+
+@pytest.mark.parametrize("T", [3, 900])
+def test_qk_norm_rope_in_place_in_a_projection(T):
+    """q and k as parts of one buffer, written back there; v and the rest keep their bits; no weights; positions outside
+    the table give NaN in the rotated part alone."""
+    _say("qk_norm_rope in place", T)
+    g = np.random.default_rng(T)
+    Hq, Hk, D, Rd, off = 12, 4, 128, 64, 64
+    buf = _bf16(R.bf16(g.normal(0, 1, (T, (Hq + 2 * Hk) * D + 16))))
+    before = _np(buf)
+    q = buf[:, :Hq * D].view(T, Hq, D)
+    k = buf[:, Hq * D:(Hq + Hk) * D].view(T, Hk, D)
+    pos = g.integers(0, 30, T).astype(np.int32)
+    pos[0], pos[1] = -1, 30
+    cs = _table(30, Rd)
+    qn, kn = _np(q), _np(k)
+    A.qk_norm_rope(q, k, None, None, _gpu(pos), _gpu(cs), rot_offset=off, eps=0.01, q_out=q, k_out=k)
+    _check_rope(q, qn, None, pos, cs, off, False, 0.01)
+    _check_rope(k, kn, None, pos, cs, off, False, 0.01)
+    assert np.isnan(_np(q)[:2, :, off:]).all() and not np.isnan(_np(q)[:2, :, :off]).any()
+    assert np.array_equal(_np(buf)[:, (Hq + Hk) * D:], before[:, (Hq + Hk) * D:])
+
+
+def test_qk_norm_rope_heads_first_and_zero_rows():
+    """A cache in [heads, rows, D] order as the output; a zero head gives zeros, an infinite or NaN one NaN."""
+    _say("qk_norm_rope heads first")
+    g = np.random.default_rng(2)
+    T, Hq, Hk, D = 20, 4, 2, 64
+    q, k = R.bf16(g.normal(0, 1, (T, Hq, D))), R.bf16(g.normal(0, 1, (T, Hk, D)))
+    q[3, 1], q[4, 0, 2], k[5, 1, 7] = 0, np.nan, np.inf
+    cs, pos = _table(T, D), np.arange(T, dtype=np.int32)
+    cache = torch.full((Hk, 100, D), 5.0, dtype=BF, device="cuda")
+    qo, _ = A.qk_norm_rope(_bf16(q), _bf16(k), None, None, _gpu(pos), _gpu(cs), k_out=cache[:, 40:60].transpose(0, 1))
+    _check_rope(qo, q, None, pos, cs, 0, False, 1e-6)
+    assert np.all(_np(qo)[3, 1] == 0) and np.isnan(_np(qo)[4, 0]).all()
+    kk = np.delete(np.arange(T), 5)
+    _check_rope(cache[:, 40:60].transpose(0, 1)[torch.from_numpy(kk).cuda()], k[kk], None, pos[kk], cs, 0, False, 1e-6)
+    assert torch.all(cache[:, :40] == 5) and torch.all(cache[:, 60:] == 5)
+
+
+# ---------------------------------------------------------------- attention
+def _check_attention(out, lse, q, k, v, seqs, scale, causal):
+    D = q.shape[2]
+    ref, rl, mag, dot = R.attention(q, k, v, seqs, scale, causal)
+    y, l = _np(out), None if lse is None else _np(lse)
+    for q0, lq, _, lk in seqs:
+        r, o, m = ref[q0:q0 + lq], y[q0:q0 + lq], mag[q0:q0 + lq]
+        assert np.array_equal(np.isnan(o), np.isnan(r))
+        assert np.array_equal(np.isinf(o), np.isinf(r))
+        fin = np.isfinite(r) & np.isfinite(m)
+        d = (D + 4) * 2.0 ** -23 * dot[q0:q0 + lq]
+        tol = U * np.abs(r) + (2 * U + 2 * np.expm1(d)[..., None] + (lk + 64) * 2.0 ** -23) * m + 1e-38
+        assert np.all(np.abs(o - r)[fin] <= tol[fin]), f"worst {np.max(np.abs(o - r)[fin] / tol[fin]):.3f} of its bound"
+        assert np.all(o[np.isinf(r)] == r[np.isinf(r)])
+        if l is not None:
+            a, b = l[q0:q0 + lq], rl[q0:q0 + lq]
+            empty = b == -np.inf
+            assert np.array_equal(a == -np.inf, empty)
+            ok = np.isfinite(b)
+            # the sum of rounded weights: u; the scores: d; the maximum and the logarithm in float32
+            assert np.all(np.abs(a - b)[ok] <= (2 * U + d + (lk + 64) * 2.0 ** -23 + 2.0 ** -21 * (1 + np.abs(b)))[ok])
+
+
+def _seqs(lq, lk=None, room=None):
+    """Packed queries; keys packed alike, or in a cache of `room` rows per sequence."""
+    q0 = np.concatenate([[0], np.cumsum(lq)])
+    if lk is None:
+        return q0, [(int(a), n, int(a), n) for a, n in zip(q0, lq)]
+    return q0, [(int(a), n, b * room, m) for b, (a, n, m) in enumerate(zip(q0, lq, lk))]
+
+
+def _run(q, k, v, q0, seqs, cache, causal=True, scale=None, **kw):
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    lse = torch.full(q.shape[:2], 3.0, device="cuda")
+    if cache:
+        kw.update(kv_start=i32([s[2] for s in seqs]), kv_len=i32([s[3] for s in seqs]))
+        kw.setdefault("max_kv", max([s[3] for s in seqs] + [0]))
+    mq = max([s[1] for s in seqs] + [0])
+    return A.attention(q, k, v, i32(q0), mq, causal=causal, scale=scale, lse=lse, **kw), lse
+
+
+CASES = [
+    # lq, lk (None: prompts), Hq, Hkv, D
+    ([1], None, 1, 1, 64), ([2], None, 4, 2, 128), ([31], None, 2, 2, 64), ([33], None, 8, 2, 128), ([64], None, 3, 1, 64),
+    ([65], None, 5, 1, 128), ([129], None, 4, 4, 128), ([200], None, 2, 1, 256), ([3, 0, 1, 70, 0, 128, 17], None, 4, 2, 64),
+    ([150, 1, 90], None, 6, 2, 128), ([5, 66], None, 2, 1, 256), ([300], None, 2, 1, 64),
+    # single tokens over caches of any length, an empty one among them
+    ([1, 1, 1, 1, 1], [1, 31, 0, 65, 300], 4, 1, 128), ([1, 1, 1], [700, 33, 128], 8, 8, 64), ([1, 1], [513, 64], 16, 2, 256),
+    ([1], [2600], 4, 1, 128), ([1, 0, 1], [100, 50, 1], 32, 2, 128), ([1, 1], [200, 129], 40, 1, 64), ([1], [97], 20, 2, 256),
+    # chunks after a prefix; more queries than keys; no keys at all
+    ([7, 40], [70, 300], 4, 2, 128), ([100, 3], [160, 3], 2, 1, 64), ([20, 60], [5, 0], 4, 2, 128), ([2, 4], [300, 1], 4, 2, 128),
+    ([40], [1500], 2, 2, 128), ([3], [900], 10, 2, 256), ([130], [64], 2, 1, 64), ([5, 5], [600, 2], 6, 2, 64),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lq,lk,Hq,Hkv,D", CASES)
+def test_attention(lq, lk, Hq, Hkv, D, causal):
+    _say("attention", lq, lk, Hq, Hkv, D, causal)
+    g = np.random.default_rng(sum(lq) * 31 + D + Hq)
+    room = max(lk) + 3 if lk else 0
+    q0, seqs = _seqs(lq, lk, room)
+    rows = len(lq) * room if lk else sum(lq)
+    q = R.bf16(g.normal(0, 2, (sum(lq), Hq, D)))
+    k, v = R.bf16(g.normal(0, 1, (rows, Hkv, D))), R.bf16(g.normal(0, 1, (rows, Hkv, D)))
+    out, lse = _run(_bf16(q), _bf16(k), _bf16(v), q0, seqs, lk is not None, causal)
+    _check_attention(out, lse, q, k, v, seqs, D ** -0.5, causal)
+
+
+@pytest.mark.parametrize("lq,lk,Hq,Hkv,D", [([70, 20], None, 4, 2, 128), ([1, 1, 1], [40, 300, 1], 8, 2, 128),
+                                           ([9], [200], 2, 1, 64), ([150], None, 1, 1, 256)])
+def test_attention_strides(lq, lk, Hq, Hkv, D):
+    """q, k and v inside one projection, or a cache in [heads, rows, D] order; an output with its heads apart; rows of
+    no sequence keep what they hold."""
+    _say("attention strides", lq, lk, D)
+    g = np.random.default_rng(D + Hq)
+    T = sum(lq)
+    lead, tail = 2, 3  # rows before the first and after the last sequence
+    if lk is None:
+        buf = _bf16(R.bf16(g.normal(0, 1, (T + lead + tail, (Hq + 2 * Hkv) * D + 8))))
+        part = lambda a, h: buf[:, a * D:(a + h) * D].view(T + lead + tail, h, D)  # noqa: E731
+        q, k, v = part(0, Hq), part(Hq, Hkv), part(Hq + Hkv, Hkv)
+        seqs, a = [], lead
+        for n in lq:
+            seqs.append((a, n, a, n))
+            a += n
+    else:
+        room = max(lk) + 5
+        q = _bf16(R.bf16(g.normal(0, 2, (T + lead + tail, Hq, D))))
+        k = _bf16(R.bf16(g.normal(0, 1, (Hkv, len(lk) * room, D)))).transpose(0, 1)
+        v = _bf16(R.bf16(g.normal(0, 1, (len(lk) * room, Hkv, D + 8))))[..., :D]
+        seqs, a = [], lead
+        for b, (n, m) in enumerate(zip(lq, lk)):
+            seqs.append((a, n, b * room + 2, m))
+            a += n
+    out = torch.full((T + lead + tail, Hq, 2 * D), 9.0, dtype=BF, device="cuda")
+    _, lse = _run(q, k, v, [s[0] for s in seqs] + [lead + T], seqs, lk is not None, out=out[..., :D])
+    _check_attention(out[..., :D], lse, _np(q), _np(k), _np(v), seqs, D ** -0.5, True)
+    assert torch.all(out[..., D:] == 9) and torch.all(out[:lead] == 9) and torch.all(out[lead + T:] == 9)
+    assert torch.all(lse[:lead] == 3) and torch.all(lse[lead + T:] == 3)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 2.0 ** 100])
+@pytest.mark.parametrize("lq,lk,G,D", [([100], None, 1, 128), ([40], None, 4, 64), ([1, 1], [70, 33], 4, 128),
+                                       ([3], [100], 2, 128), ([2], [600], 4, 256), ([60, 60], [700, 61], 1, 128)])
+def test_attention_hidden_values(lq, lk, G, D, bad):
+    """What a row must not see does not reach it, whatever it holds: cache rows past a sequence's end, and later keys
+    of a causal prompt; rows that do see it show it as the formula does."""
+    _say("attention hidden", lq, lk, D, bad)
+    g = np.random.default_rng(11)
+    room = max(lk) + 40 if lk else 0
+    q0, seqs = _seqs(lq, lk, room)
+    rows = len(lq) * room if lk else sum(lq)
+    q = R.bf16(g.normal(0, 1, (sum(lq), 2 * G, D)))
+    k, v = R.bf16(g.normal(0, 1, (rows, 2, D))), R.bf16(g.normal(0, 1, (rows, 2, D)))
+    for _, n, k0, m in seqs:
+        if lk:
+            k[k0 + m:k0 + room], v[k0 + m:k0 + room] = bad, bad
+        if n > 2:                      # a value that only the last two queries see
+            v[k0 + m - 2, 1, 5] = bad
+            v[k0 + m - 2, 0, 6] = -bad
+    out, lse = _run(_bf16(q), _bf16(k), _bf16(v), q0, seqs, lk is not None)
+    _check_attention(out, lse, q, k, v, seqs, D ** -0.5, True)
+
+
+def test_attention_hidden_keys_and_bad_queries():
+    """A NaN or infinite key that only later queries see; a NaN query spoils its own row alone."""
+    _say("attention hidden keys")
+    g = np.random.default_rng(12)
+    q = R.bf16(g.normal(0, 1, (90, 4, 64)))
+    k, v = R.bf16(g.normal(0, 1, (90, 2, 64))), R.bf16(g.normal(0, 1, (90, 2, 64)))
+    k[80, 0], k[85, 1, 3], q[20, 2] = np.nan, np.inf, np.nan
+    out, _ = _run(_bf16(q), _bf16(k), _bf16(v), [0, 90], [(0, 90, 0, 90)], False)
+    y = _np(out)
+    assert np.isnan(y[20, 2]).all() and np.isnan(y[80:, :2]).all()
+    y[20, 2] = 0
+    assert not np.isnan(y[:80]).any() and not np.isnan(y[:85, 2:]).any()
+
+
+def test_attention_extreme_scores():
+    """Scores of +-1e4 and rows whose scores rise tile by tile: the running maximum carries them."""
+    _say("attention extreme scores")
+    g = np.random.default_rng(13)
+    D, L = 64, 500
+    k = R.bf16(g.normal(0, 1, (L, 1, D)))
+    k[:, 0, 0] = R.bf16(np.linspace(-60, 60, L))
+    v = R.bf16(g.normal(0, 1, (L, 1, D)))
+    q = R.bf16(g.normal(0, 1, (8, 1, D)))
+    q[:, 0, 0] = [1, -1, 16, -16, 100, -100, 1e3, 0]
+    for lq, cache in (([1] * 8, True), ([8], True)):
+        seqs = [(i, 1, 0, L) for i in range(8)] if len(lq) == 8 else [(0, 8, 0, L)]
+        out, lse = _run(_bf16(q), _bf16(k), _bf16(v), [s[0] for s in seqs] + [8], seqs, cache)
+        _check_attention(out, lse, q, k, v, seqs, D ** -0.5, True)
+
+
+@pytest.mark.parametrize("lq,lk", [(1, 3000), (12, 2000), (90, 1500)])
+def test_attention_long_cache_past_32_bits(lq, lk):
+    """A cache of more than 2^31 elements: sequences at its ends and across element 2^31."""
+    Hkv, D = 8, 128
+    rows = (1 << 21) + 9000
+    _say("attention long cache", lq, lk)
+    k = torch.empty(rows, Hkv, D, dtype=BF, device="cuda")
+    v = torch.empty(rows, Hkv, D, dtype=BF, device="cuda")
+    starts = [0, (1 << 21) - lk // 2, rows - lk]
+    for s in starts:
+        k[s:s + lk].normal_()
+        v[s:s + lk].normal_()
+    q = torch.randn(3 * lq, 8, D, device="cuda").to(BF)
+    seqs = [(b * lq, lq, s, lk) for b, s in enumerate(starts)]
+    out, lse = _run(q, k, v, [0, lq, 2 * lq, 3 * lq], seqs, True)
+    for q0, n, s, m in seqs:
+        sub = [(0, n, 0, m)]
+        _check_attention(out[q0:q0 + n], lse[q0:q0 + n], _np(q[q0:q0 + n]), _np(k[s:s + m]), _np(v[s:s + m]), sub,
+                         D ** -0.5, True)
+
+
+def test_attention_ranges_are_cut_to_the_tensors():
+    """cu_q, kv_start and kv_len that point outside read and write nothing there; lengths past max_q and max_kv are cut."""
+    _say("attention ranges")
+    g = np.random.default_rng(14)
+    q = R.bf16(g.normal(0, 1, (40, 2, 64)))
+    k, v = R.bf16(g.normal(0, 1, (100, 1, 64))), R.bf16(g.normal(0, 1, (100, 1, 64)))
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = torch.full((40, 2, 64), 9.0, dtype=BF, device="cuda")
+    A.attention(_bf16(q), _bf16(k), _bf16(v), i32([-5, 10, 10, 30, 2000000000]), 40, out=out, causal=False,
+                kv_start=i32([-7, 0, 90, 99]), kv_len=i32([30, -3, 1 << 30, 50]), max_kv=100)
+    ref = [(0, 10, 0, 30), (10, 20, 90, 10), (30, 10, 99, 1)]
+    _check_attention(out, None, q, k, v, ref, 0.125, False)
+    out.fill_(9.0)
+    A.attention(_bf16(q), _bf16(k), _bf16(v), i32([0, 40]), 25, out=out, causal=False, kv_start=i32([0]),
+                kv_len=i32([100]), max_kv=60)
+    _check_attention(out, None, q, k, v, [(0, 25, 0, 60)], 0.125, False)
+    assert torch.all(out[25:] == 9)
+
+
+def test_attention_many_sequences():
+    """More sequences than a wave looks up at once, most of them of a few tokens."""
+    _say("attention many sequences")
+    g = np.random.default_rng(15)
+    lq = [int(n) for n in g.integers(0, 6, 200)]
+    lq[7], lq[150] = 140, 133
+    q0, seqs = _seqs(lq)
+    q = R.bf16(g.normal(0, 1, (sum(lq), 2, 64)))
+    k, v = R.bf16(g.normal(0, 1, (sum(lq), 1, 64))), R.bf16(g.normal(0, 1, (sum(lq), 1, 64)))
+    out, lse = _run(_bf16(q), _bf16(k), _bf16(v), q0, seqs, False)
+    _check_attention(out, lse, q, k, v, seqs, 0.125, True)
+
+
+# ---------------------------------------------------------------- streams, graphs, repeats
+def _three(st):
+    y = A.fp8_linear(st["x"], st["w"], st["s"], y=st["y"], ws=st["ws1"])
+    qkv = y.view(-1, 6, 64)
+    A.qk_norm_rope(qkv[:, :4], qkv[:, 4:5], st["qw"], None, st["pos"], st["cs"], q_out=st["q"], k_out=st["k"])
+    return A.attention(st["q"], st["k"], qkv[:, 5:], st["cu"], 60, out=st["out"], lse=st["lse"], ws=st["ws2"])
+
+
+def _three_state(T=100):
+    g = np.random.default_rng(T)
+    codes, s, _ = _weights(g, 384, 512, "e8m0")
+    st = dict(x=_bf16(g.normal(0, 1, (T, 512))), w=_gpu(codes), s=_gpu(s), qw=_gpu(np.float32(g.normal(1, 0.1, 64))),
+              pos=_gpu(np.arange(T, dtype=np.int32)), cs=_gpu(_table(T, 64)),
+              cu=torch.tensor([0, 40, T], dtype=torch.int32, device="cuda"),
+              y=torch.empty(T, 384, dtype=BF, device="cuda"), q=torch.empty(T, 4, 64, dtype=BF, device="cuda"),
+              k=torch.empty(T, 1, 64, dtype=BF, device="cuda"), out=torch.empty(T, 4, 64, dtype=BF, device="cuda"),
+              lse=torch.empty(T, 4, device="cuda"), ws1=A.fp8_linear_workspace(T, 384, 512))
+    st["ws2"] = A.attention_workspace(st["q"], st["k"], 2, 60, 60)
+    return st
+
+
+def test_graph_replay_matches_eager():
+    _say("graph")
+    st = _three_state()
+    want = _three(st).clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _three(st)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _three(st)
+    for i in range(4):
+        st["out"].zero_()
+        st["ws2"].fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(st["out"], want), i
+        assert torch.equal(_three(st), want)
+        torch.cuda.synchronize()
+
+
+def test_other_stream():
+    """The calls go to the caller's current stream and are ordered there."""
+    _say("stream")
+    st = _three_state()
+    want = _three(st).clone()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        st["x"].mul_(2.0)
+        st["x"].mul_(0.5)
+        st["out"].zero_()
+        got = _three(st).clone()
+    s.synchronize()
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("lq,lk,Hq,Hkv", [([1, 1], [5000, 900], 8, 2), ([50], [3000], 4, 1), ([400], None, 8, 2)])
+def test_attention_repeats_bit_for_bit(lq, lk, Hq, Hkv):
+    _say("repeat", lq, lk)
+    torch.manual_seed(0)
+    room = max(lk) if lk else 0
+    q0, seqs = _seqs(lq, lk, room)
+    rows = len(lq) * room if lk else sum(lq)
+    q = torch.randn(sum(lq), Hq, 128, device="cuda").to(BF)
+    k, v = torch.randn(rows, Hkv, 128, device="cuda").to(BF), torch.randn(rows, Hkv, 128, device="cuda").to(BF)
+    a, la = _run(q, k, v, q0, seqs, lk is not None)
+    for _ in range(3):
+        b, lb = _run(q, k, v, q0, seqs, lk is not None)
+        assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+# ---------------------------------------------------------------- refusals of the binding
+def test_binding_refusals():
+    q, k = torch.zeros(4, 2, 64, dtype=BF, device="cuda"), torch.zeros(4, 1, 64, dtype=BF, device="cuda")
+    cu = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    one = torch.ones(1, dtype=torch.int32, device="cuda")
+    for args, kw in [((q.float(), k, k, cu, 4), {}), ((q, k, k[:3], cu, 4), {}), ((q, k, k, cu.long(), 4), {}),
+                     ((q, k, k, cu.cpu(), 4), {}), ((q, k, k, cu, 4), dict(kv_start=one)), ((q, k[..., :32], k[..., :32], cu, 4), {}),
+                     ((q, k, k, cu, 4), dict(kv_start=one, kv_len=torch.ones(2, dtype=torch.int32, device="cuda"))),
+                     ((q, k, k, cu, 4), dict(out=q[:3])), ((q, k, k, cu, 4), dict(lse=torch.zeros(4, 3, device="cuda"))),
+                     ((q[0], k, k, cu, 4), {}), ((q, k, k, cu, 4), dict(ws=torch.zeros(8, device="cuda")))]:
+        with pytest.raises(ValueError):
+            A.attention(*args, **kw)
+    for bad in (5, -1):
+        with pytest.raises(A.MoeError):
+            A.attention(q, k, k, cu, bad)
+    with pytest.raises(A.MoeError):
+        A.attention(torch.zeros(4, 3, 64, dtype=BF, device="cuda"), torch.zeros(4, 2, 64, dtype=BF, device="cuda"),
+                    torch.zeros(4, 2, 64, dtype=BF, device="cuda"), cu, 4)
+    x, w, s = torch.zeros(4, 64, dtype=BF, device="cuda"), torch.zeros(8, 64, dtype=torch.uint8, device="cuda"), \
+        torch.zeros(1, 1, dtype=torch.uint8, device="cuda")
+    for args, kw in [((x.float(), w, s), {}), ((x[:, :32], w, s), {}), ((x, w.t().contiguous().t(), s), {}),
+                     ((x, w, s.int()), {}), ((x, w, torch.zeros(2, 1, dtype=torch.uint8, device="cuda")), {}),
+                     ((x, w, s), dict(y=torch.zeros(4, 9, dtype=BF, device="cuda"))),
+                     ((x.t().contiguous().t(), w, s), {}), ((x, w, s), dict(ws=torch.zeros(4096, dtype=torch.uint8)))]:
+        with pytest.raises(ValueError):
+            A.fp8_linear(*args, **kw)
+    with pytest.raises(A.MoeError):
+        A.fp8_linear(x, w, s, ws=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    pos, cs = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(8, 64, device="cuda")
+    for args, kw in [((q, k, None, None, None, cs), {}), ((q, k, cs[0, :32], None, pos, cs), {}),
+                     ((q, k, None, None, pos[:3], cs), {}), ((q, k[:3], None, None, pos, cs), {}),
+                     ((q, k, None, None, pos, cs.double()), {}), ((q, k, None, None, pos, cs), dict(q_out=k))]:
+        with pytest.raises(ValueError):
+            A.qk_norm_rope(*args, **kw)
+    with pytest.raises(A.MoeError):
+        A.qk_norm_rope(q, k, None, None, pos, cs, rot_offset=8)
+
+
+def test_no_tokens():
+    """Empty batches are no-ops."""
+    e = lambda *s: torch.empty(*s, dtype=BF, device="cuda")  # noqa: E731
+    z = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert A.fp8_linear(e(0, 64), torch.zeros(8, 64, dtype=torch.uint8, device="cuda"),
+                        torch.zeros(1, 1, dtype=torch.uint8, device="cuda")).shape == (0, 8)
+    assert A.qk_norm_rope(e(0, 2, 64), e(0, 1, 64), None, None, None, None)[0].shape == (0, 2, 64)
+    assert A.attention(e(0, 2, 64), e(0, 1, 64), e(0, 1, 64), z, 0).shape == (0, 2, 64)
