@@ -14,9 +14,12 @@ library, and a non-zero status raises MoeError.  There is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import struct
+
+import torch
 
 from . import binding as B
-from .binding import MoeError, _check, _dev, _ptr, _stream, _torch  # noqa: F401
+from .binding import MoeError, _check  # noqa: F401
 
 MOE_SCALE_E8M0 = 0  # one byte per block, value 2^(e - 127)
 MOE_SCALE_F32 = 1   # one float32 per block
@@ -49,7 +52,7 @@ def lib() -> ctypes.CDLL:
     if _typed is L:
         return L
     i32, i64, sz, vp, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
-    heads, attn = ctypes.POINTER(moe_heads), ctypes.POINTER(moe_attn)
+    heads = attn = vp  # a struct by reference, or its packed bytes
     sig = {
         "moe_fp8_linear_workspace_size": (sz, [i32, i32, i32]),
         "moe_fp8_linear": (ctypes.c_int, [vp, i64, i32, i32, vp, vp, i32, i32, vp, i64, vp, sz, vp]),
@@ -68,60 +71,80 @@ def lib() -> ctypes.CDLL:
 
 
 # ---------------------------------------------------------------- argument checks
-def _on(t, dtypes, name, device=None):
-    """A device tensor of one of the dtypes, on `device` where one is given."""
+# A call of a few microseconds on the GPU should not wait for its checks: each
+# looks at a tensor once, and the structs are packed in one go.
+_BF16 = (torch.bfloat16, torch.int16)
+_I32, _F32, _U8 = (torch.int32,), (torch.float32,), (torch.uint8,)
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_SCALE = (torch.uint8, torch.float8_e8m0fnu, torch.float32)
+_HEADS = struct.Struct("=Qqq")
+_ATTN = struct.Struct("=I9ifi" + 4 * "Qqq" + "4Q")
+_NO_HEADS = _HEADS.pack(0, 0, 0)
+_stream = torch._C._cuda_getCurrentRawStream
+_device = torch._C._cuda_getDevice
+
+
+def _refuse(t, dtypes, name, dev):
+    """The error of a tensor that failed a check of its device or type."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.dtype not in (dtypes if isinstance(dtypes, tuple) else (dtypes,)):
+    if t.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {dtypes}, got {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return t
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
 
 
-def _current(t, name):
-    """The calls go to the current device's stream: the tensors must be there."""
-    cur = _torch().cuda.current_device()
-    if t.device.index != cur:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
-    return t.device
+def _current(t, dtypes, name):
+    """The device of the call: t's, which must be the current one."""
+    dev = t.get_device()
+    if dev < 0 or t.dtype not in dtypes:
+        _refuse(t, dtypes, name, dev)
+    if dev != _device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_device()}")
+    return dev
 
 
-def _flat(t, dtypes, name, device, shape=None):
-    _on(t, dtypes, name, device)
+def _flat(t, dtypes, name, dev, shape=None):
+    """The address of a contiguous tensor."""
+    if t.dtype not in dtypes or t.get_device() != dev:
+        _refuse(t, dtypes, name, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+    return t.data_ptr()
 
 
-def _bf16():
-    torch = _torch()
-    return (torch.bfloat16, torch.int16)
-
-
-def _heads(t, name, device, shape=None):
-    """A [rows, heads, head_dim] tensor as a moe_heads."""
-    _on(t, _bf16(), name, device)
-    if t.dim() != 3:
+def _heads(t, name, dev, shape=None):
+    """Address, row stride and head stride of a [rows, heads, head_dim] tensor."""
+    if t.dtype not in _BF16 or t.get_device() != dev:
+        _refuse(t, _BF16, name, dev)
+    have = t.shape
+    if len(have) != 3:
         raise ValueError(f"{name} must have three dimensions (rows, heads, head_dim)")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if shape is not None and have != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(have)}")
+    rows, heads, d = have
+    row, head, one = t.stride()
+    if one != 1 and d > 1:
         raise ValueError(f"{name} must have unit stride inside a head")
     # a dimension of one entry may carry any stride
-    d = max(t.shape[2], 8)
-    head = t.stride(1) if t.shape[1] > 1 else d
-    row = t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1) * d
-    return moe_heads(t.data_ptr(), row, head)
+    if heads <= 1:
+        head = max(d, 8)
+    if rows <= 1:
+        row = max(heads, 1) * max(d, 8)
+    return t.data_ptr(), row, head
 
 
-def _workspace(ws, need, device):
-    torch = _torch()
-    if ws is None:
-        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
-    return _flat(ws, torch.uint8, "ws", device)
+def _rows(t, name, dev, shape):
+    """Address and row stride of a [rows, columns] tensor."""
+    if t.dtype not in _BF16 or t.get_device() != dev:
+        _refuse(t, _BF16, name, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    row, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    return t.data_ptr(), row if shape[0] > 1 else -(-shape[1] // 8) * 8
 
 
 # ---------------------------------------------------------------- fp8 linear
@@ -131,7 +154,6 @@ def fp8_linear_workspace_size(T: int, N: int, K: int) -> int:
 
 def fp8_linear_workspace(T: int, N: int, K: int, device="cuda"):
     """A workspace that fp8_linear takes for up to T tokens of this weight."""
-    torch = _torch()
     return torch.empty(max(fp8_linear_workspace_size(T, N, K), 256), dtype=torch.uint8, device=device)
 
 
@@ -141,28 +163,26 @@ def fp8_linear(x, w, w_scale, y=None, ws=None):
 
     w is float8_e4m3fn or its bytes (uint8); w_scale is float8_e8m0fnu or its
     bytes (uint8), or float32.  Rows of x and y may be strided."""
-    torch = _torch()
-    _on(x, _bf16(), "x")
-    dev = _current(x, "x")
-    if x.dim() != 2 or w.dim() != 2 or w.shape[1] != x.shape[1]:
-        raise ValueError(f"x [T, K] and w [N, K] do not fit: {tuple(x.shape)}, {tuple(w.shape)}")
-    T, K = x.shape
-    N = w.shape[0]
-    _flat(w, (torch.uint8, torch.float8_e4m3fn), "w", dev)
-    _flat(w_scale, (torch.uint8, torch.float8_e8m0fnu, torch.float32), "w_scale", dev, (-(-N // 128), -(-K // 128)))
+    dev = _current(x, _BF16, "x")
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w must have two dimensions")
+    T, K = shape = x.shape
+    N, Kw = w.shape
+    if K != Kw:
+        raise ValueError(f"x [T, K] and w [N, K] do not fit: {tuple(shape)}, {(N, Kw)}")
     if y is None:
-        y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
-    _on(y, _bf16(), "y", dev)
-    if tuple(y.shape) != (T, N):
-        raise ValueError(f"y must have shape {(T, N)}, got {tuple(y.shape)}")
-    for t, name in ((x, "x"), (y, "y")):
-        if t.shape[1] > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name} must have unit stride along its rows")
-    ws = _workspace(ws, fp8_linear_workspace_size(T, N, K), dev)
+        y = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+    xp, xs = _rows(x, "x", dev, shape)
+    yp, ys = _rows(y, "y", dev, (T, N))
+    wp = _flat(w, _E4M3, "w", dev)
+    sp = _flat(w_scale, _SCALE, "w_scale", dev, (-(-N // 128), -(-K // 128)))
+    if ws is None:
+        ws = fp8_linear_workspace(T, N, K, x.device)
     kind = MOE_SCALE_F32 if w_scale.dtype == torch.float32 else MOE_SCALE_E8M0
-    xs, ys = (x.stride(0), y.stride(0)) if T > 1 else (-(-K // 8) * 8, N)
-    _check("moe_fp8_linear", lib().moe_fp8_linear(x.data_ptr(), xs, T, K, w.data_ptr(), w_scale.data_ptr(), kind, N,
-                                                  y.data_ptr(), ys, ws.data_ptr(), ws.numel(), _stream()))
+    st = lib().moe_fp8_linear(xp, xs, T, K, wp, sp, kind, N, yp, ys, _flat(ws, _U8, "ws", dev), ws.numel(),
+                              _stream(dev))
+    if st:
+        raise MoeError("moe_fp8_linear", st)
     return y
 
 
@@ -175,54 +195,54 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, *, rot_offset=0, 
     q_weight, k_weight: float32 [D] or None; positions: int32 [T]; cos_sin:
     float32 [n_positions, rot_dim], the cosines of the rot_dim / 2 pairs, then
     their sines.  positions and cos_sin None: no rotation."""
-    torch = _torch()
-    _on(q, _bf16(), "q")
-    dev = _current(q, "q")
+    dev = _current(q, _BF16, "q")
     hq = _heads(q, "q", dev)
-    T, Hq, D = q.shape
-    q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev) if q_out is None else q_out
-    hqo = _heads(q_out, "q_out", dev, (T, Hq, D))
-    hk, hko, Hk = moe_heads(), moe_heads(), 0
+    T, Hq, D = shape = q.shape
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    hq, hqo = _HEADS.pack(*hq), _HEADS.pack(*_heads(q_out, "q_out", dev, shape))
+    hk = hko = _NO_HEADS
+    Hk = 0
     if k is not None:
-        Hk = k.shape[1]
-        hk = _heads(k, "k", dev, (T, Hk, D))
-        k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=dev) if k_out is None else k_out
-        hko = _heads(k_out, "k_out", dev, (T, Hk, D))
-    for wt, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if wt is not None:
-            _flat(wt, torch.float32, name, dev, (D,))
+        hk = _heads(k, "k", dev)
+        kshape = k.shape
+        Hk = kshape[1]
+        if kshape[0] != T or kshape[2] != D:
+            raise ValueError(f"k must have shape {(T, Hk, D)}, got {tuple(kshape)}")
+        if k_out is None:
+            k_out = torch.empty(kshape, dtype=torch.bfloat16, device=q.device)
+        hk, hko = _HEADS.pack(*hk), _HEADS.pack(*_heads(k_out, "k_out", dev, kshape))
+    qw = None if q_weight is None else _flat(q_weight, _F32, "q_weight", dev, (D,))
+    kw = None if k_weight is None else _flat(k_weight, _F32, "k_weight", dev, (D,))
     P = R = 0
+    pos = cs = None
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [n_positions, rot_dim]")
-        P, R = _flat(cos_sin, torch.float32, "cos_sin", dev).shape
         if positions is None:
             raise ValueError("cos_sin needs positions")
-        _flat(positions, torch.int32, "positions", dev, (T,))
-    _check("moe_qk_norm_rope", lib().moe_qk_norm_rope(
-        ctypes.byref(hq), Hq, ctypes.byref(hk), Hk, T, D, _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions),
-        _ptr(cos_sin), P, R, rot_offset, int(bool(interleaved)), ctypes.byref(hqo), ctypes.byref(hko), _stream()))
+        P, R = cos_sin.shape
+        cs = _flat(cos_sin, _F32, "cos_sin", dev)
+        pos = _flat(positions, _I32, "positions", dev, (T,))
+    st = lib().moe_qk_norm_rope(hq, Hq, hk, Hk, T, D, qw, kw, eps, pos, cs, P, R, rot_offset, 1 if interleaved else 0,
+                                hqo, hko, _stream(dev))
+    if st:
+        raise MoeError("moe_qk_norm_rope", st)
     return q_out, k_out
 
 
 # ---------------------------------------------------------------- attention
-def _attn(q_shape, kv_shape, n_seqs, max_q, max_kv):
-    """A descriptor with the shape fields set."""
-    a = moe_attn()
-    a.abi_version = B.MOE_ABI_VERSION
-    a.q_rows, a.q_heads, a.head_dim = q_shape
-    a.kv_rows, a.kv_heads = kv_shape[0], kv_shape[1]
-    a.n_seqs, a.max_q, a.max_kv = n_seqs, max_q, max_kv
-    return a
-
-
 def attention_workspace_size(q, k, n_seqs: int, max_q: int, max_kv: int) -> int:
     """Bytes attention() needs for q and k of these shapes and bounds."""
-    return int(lib().moe_attention_workspace_size(ctypes.byref(_attn(q.shape, k.shape, n_seqs, max_q, max_kv))))
+    a = moe_attn()
+    a.abi_version = B.MOE_ABI_VERSION
+    a.q_rows, a.q_heads, a.head_dim = q.shape
+    a.kv_rows, a.kv_heads = k.shape[0], k.shape[1]
+    a.n_seqs, a.max_q, a.max_kv = n_seqs, max_q, max_kv
+    return int(lib().moe_attention_workspace_size(ctypes.byref(a)))
 
 
 def attention_workspace(q, k, n_seqs: int, max_q: int, max_kv: int):
-    torch = _torch()
     return torch.empty(max(attention_workspace_size(q, k, n_seqs, max_q, max_kv), 256), dtype=torch.uint8,
                        device=q.device)
 
@@ -238,42 +258,39 @@ def attention(q, k, v, cu_q, max_q: int, *, kv_start=None, kv_len=None, max_kv=N
     rows kv_start[b] .. kv_start[b] + kv_len[b] - 1 of a cache, the new rows included.
     scale: default D ** -0.5.  lse: float32 [q_rows, Hq] to fill, or None.  Rows
     of out that belong to no sequence are left as they are (new: undefined)."""
-    torch = _torch()
-    _on(q, _bf16(), "q")
-    dev = _current(q, "q")
+    dev = _current(q, _BF16, "q")
     hq = _heads(q, "q", dev)
     hk = _heads(k, "k", dev)
-    hv = _heads(v, "v", dev, k.shape)
-    if k.shape[2] != q.shape[2]:
-        raise ValueError(f"q and k have different head sizes: {q.shape[2]}, {k.shape[2]}")
+    qshape, kshape = q.shape, k.shape
+    hv = _heads(v, "v", dev, kshape)
+    Tq, Hq, D = qshape
+    Tk, Hk, Dk = kshape
+    if Dk != D:
+        raise ValueError(f"q and k have different head sizes: {D}, {Dk}")
     if cu_q.dim() != 1 or cu_q.numel() < 1:
         raise ValueError("cu_q must be [n_seqs + 1]")
     n_seqs = cu_q.numel() - 1
-    _flat(cu_q, torch.int32, "cu_q", dev)
-    if (kv_start is None) != (kv_len is None):
+    cu = _flat(cu_q, _I32, "cu_q", dev)
+    start = length = lp = 0
+    if kv_start is not None and kv_len is not None:
+        start = _flat(kv_start, _I32, "kv_start", dev, (n_seqs,))
+        length = _flat(kv_len, _I32, "kv_len", dev, (n_seqs,))
+    elif kv_start is not None or kv_len is not None:
         raise ValueError("kv_start and kv_len go together")
-    if kv_start is not None:
-        _flat(kv_start, torch.int32, "kv_start", dev, (n_seqs,))
-        _flat(kv_len, torch.int32, "kv_len", dev, (n_seqs,))
     if lse is not None:
-        _flat(lse, torch.float32, "lse", dev, q.shape[:2])
-    out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if out is None else out
+        lp = _flat(lse, _F32, "lse", dev, (Tq, Hq))
+    if out is None:
+        out = torch.empty(qshape, dtype=torch.bfloat16, device=q.device)
+    ho = _heads(out, "out", dev, qshape)
     if max_kv is None:
-        max_kv = min(max_q, k.shape[0]) if kv_start is None else k.shape[0]
-    a = _attn(q.shape, k.shape, n_seqs, max_q, max_kv)
-    a.causal = int(bool(causal))
-    a.scale = q.shape[2] ** -0.5 if scale is None else scale
-    a.q, a.k, a.v, a.out = hq, hk, hv, _heads(out, "out", dev, q.shape)
-    a.cu_q = cu_q.data_ptr()
-    if kv_start is not None:
-        a.kv_start, a.kv_len = kv_start.data_ptr(), kv_len.data_ptr()
-    if lse is not None:
-        a.lse = lse.data_ptr()
+        max_kv = Tk if start else min(max_q, Tk)
+    a = _ATTN.pack(B.MOE_ABI_VERSION, D, Hq, Hk, n_seqs, Tq, Tk, max_q, max_kv, 1 if causal else 0,
+                   D ** -0.5 if scale is None else scale, 0, *hq, *hk, *hv, *ho, cu, start, length, lp)
     L = lib()
     if ws is None:
-        need = int(L.moe_attention_workspace_size(ctypes.byref(a)))
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    else:
-        _flat(ws, torch.uint8, "ws", dev)
-    _check("moe_attention", L.moe_attention(ctypes.byref(a), _ptr(ws), 0 if ws is None else ws.numel(), _stream()))
+        need = int(L.moe_attention_workspace_size(a))
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+    st = L.moe_attention(a, _flat(ws, _U8, "ws", dev), ws.numel(), _stream(dev))
+    if st:
+        raise MoeError("moe_attention", st)
     return out
