@@ -411,14 +411,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_rows_kernel(AttnAr
     if (key + kKeysP <= w.lk) {
 #pragma unroll
       for (int i = 0; i < kOps; ++i)
-        dma16(kr, koff[i], &to[0][1024 * (4 * i + wave)]);
+        dma16(kr, koff[i], 0, &to[0][1024 * (4 * i + wave)]);
 #pragma unroll
       for (int i = 0; i < kOps; ++i)
-        dma16(vr, voff[i], &to[1][1024 * (4 * i + wave)]);
+        dma16(vr, voff[i], 0, &to[1][1024 * (4 * i + wave)]);
     } else {
       for (int i = 0; i < kOps; ++i) {
-        dma16(kr, dma_offset<D, false>(4 * i + wave, w.lk - key, krow), &to[0][1024 * (4 * i + wave)]);
-        dma16(vr, dma_offset<D, true>(4 * i + wave, w.lk - key, vrow), &to[1][1024 * (4 * i + wave)]);
+        dma16(kr, dma_offset<D, false>(4 * i + wave, w.lk - key, krow), 0, &to[0][1024 * (4 * i + wave)]);
+        dma16(vr, dma_offset<D, true>(4 * i + wave, w.lk - key, vrow), 0, &to[1][1024 * (4 * i + wave)]);
       }
     }
   };
@@ -515,10 +515,10 @@ __global__ __launch_bounds__(64 * decode_waves<D>(), 1) void attn_token_kernel(A
     const __amdgpu_buffer_rsrc_t vr = raw_buffer(vb + key * a.v.row_stride, 0x7fffffff);
 #pragma unroll
     for (int i = 0; i < kOps; ++i)
-      dma16(kr, dma_offset<D, false>(i, w.lk - key, krow), &to[0][1024 * i]);
+      dma16(kr, dma_offset<D, false>(i, w.lk - key, krow), 0, &to[0][1024 * i]);
 #pragma unroll
     for (int i = 0; i < kOps; ++i)
-      dma16(vr, dma_offset<D, true>(i, w.lk - key, vrow), &to[1][1024 * i]);
+      dma16(vr, dma_offset<D, true>(i, w.lk - key, vrow), 0, &to[1][1024 * i]);
   };
 
   RowState<D> st;

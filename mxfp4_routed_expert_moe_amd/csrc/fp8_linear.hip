@@ -15,6 +15,7 @@
 // blocks), and W repeats its row's last 16 bytes: zero times a weight the row holds
 // anyway.  Past the end of N and T the last row is repeated and not stored.
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/moe_attention.h"
 #include "lds_dma.h"
@@ -62,8 +63,10 @@ __device__ __forceinline__ float max_abs(u32x4 w, float m) {
   return m;
 }
 
-// codes [T, Kp] (Kp = K padded to whole blocks, zeros there), scales [Kp / 128, T].
-// 16 lanes per block, 8 values each.
+// codes [kb, T, 128] (the last block padded with zeros), scales [kb, T].  Block by
+// block, so that the rows a tile kernel reads at once are contiguous: rows K
+// bytes apart would fall on few of the L2's channels.  16 lanes per block, 8
+// values each.
 template <bool F32>
 __global__ __launch_bounds__(256) void fp8_quant_kernel(const uint16_t* __restrict__ x, int64_t x_stride, int T, int K,
                                                         int kb, uint8_t* __restrict__ codes,
@@ -80,7 +83,7 @@ __global__ __launch_bounds__(256) void fp8_quant_kernel(const uint16_t* __restri
   float inv;
   const uint32_t s = block_scale<F32>(m, inv);
   const u32x2 c = {codes4(w[0], w[1], inv), codes4(w[2], w[3], inv)};
-  *reinterpret_cast<u32x2*>(codes + t * (128 * kb) + k) = c;
+  *reinterpret_cast<u32x2*>(codes + (static_cast<int64_t>(b) * T + t) * 128 + 8 * (threadIdx.x & 15)) = c;
   if ((threadIdx.x & 15) == 0) scales[static_cast<int64_t>(b) * T + t] = s;
 }
 
@@ -132,7 +135,7 @@ struct LinearArgs {
   const uint8_t* w;
   const void* w_scale;
   uint16_t* y;
-  const uint8_t* codes;    // quantised x [T, 128 kb]
+  const uint8_t* codes;    // quantised x [kb, T, 128]
   const uint32_t* scales;  // [kb, T]
   int T, N, K, kb;         // kb: blocks of K
   int n_tiles, t_tiles;
@@ -182,7 +185,7 @@ __global__ __launch_bounds__(64 * kNW) void fp8_few_kernel(LinearArgs a) {
             if (k + 8 * i < a.K && t0 + 16 * m + r < a.T) xv[u][m][i] = ld16(p + 8 * i);
           }
         } else {
-          const uint8_t* p = a.codes + static_cast<int64_t>(t) * (128 * a.kb) + k;
+          const uint8_t* p = a.codes + (static_cast<int64_t>(b) * a.T + t) * 128 + 32 * g;
           xv[u][m][0] = ld16(p);
           xv[u][m][1] = ld16(p + 16);
           sx[u][m] = a.scales[static_cast<int64_t>(b) * a.T + t];
@@ -229,114 +232,222 @@ __global__ __launch_bounds__(64 * kNW) void fp8_few_kernel(LinearArgs a) {
 }
 
 // ---------------------------------------------------------------- many tokens
-// A block holds BN rows of W and BT tokens, its waves WN x WT parts of that.  Both
-// operands come through LDS by DMA in two stages of one block of K: 16-byte
-// chunk c of a 128-byte row r sits at slot c ^ ((r / 2) mod 8), which spreads the 16
-// rows of a fragment read over all banks.  The two stages are variables of
-// their own, so that the compiler does not wait for the DMA into one before
-// it reads the other.
+// A block of eight waves holds BN rows of W and BT tokens: group 0 (waves 0 to 3)
+// the first half of the rows, group 1 the second, each wave a quarter of the
+// tokens.  Both operands come through LDS by DMA, in two stages of one block of K.
+//
+// Two waves share a SIMD, one of each group.  Were both to read their fragments
+// after the same barrier and multiply after that, the matrix cores would wait for
+// the LDS in every step; so the groups run half a step apart: while one reads the
+// fragments of a block of K into its registers, the other multiplies, and a
+// barrier swaps them.
+//
+//   phase 2 b       group 0 reads block b        group 1 multiplies block b - 1
+//   phase 2 b + 1   group 0 multiplies block b   group 1 reads block b
+//
+// Each part of a stage is refilled as soon as its readers are done, so that
+// loads are in flight at all times: the tokens X (read in both phases) and group
+// 1's rows of block b + 1 are issued in phase 2 b, group 0's rows of block b + 2 in
+// phase 2 b + 1.  The loads return in order, so a wait names how many of the
+// latest may still be out.
+//
+// Layout: rows of 128 bytes, 16-byte chunk c of row r in slot c ^ ((r / 2) mod 8),
+// which spreads the 16 rows of a fragment read over all banks.  An operand's lane
+// (r, g) holds chunks g and 4 + g of row r.  Every part is a variable of its own:
+// the compiler then knows that a DMA in flight does not write what is read.
 __device__ __forceinline__ int slot(int r, int c) { return c ^ ((r >> 1) & 7); }
 
-template <int BN, int BT, int WN, int WT, bool F32>
-__global__ __launch_bounds__(64 * WN * WT, 2) void fp8_tile_kernel(LinearArgs a) {
-  constexpr int kWaves = WN * WT;
-  constexpr int kN = BN / WN / 16, kT = BT / WT / 16;  // 16 x 16 tiles of a wave
-  constexpr int kWOps = BN / 8 / kWaves, kXOps = BT / 8 / kWaves;  // DMA instructions, 8 rows each
-  static_assert(BN / WN <= 128, "a wave's rows of W lie in one scale block");
-  struct Stage {
-    uint8_t w[BN * 128], x[BT * 128];
+template <int BN, int BT, bool F32>
+__global__ __launch_bounds__(512, 2) void fp8_tile_kernel(LinearArgs a) {
+  constexpr int kN = BN / 32, kT = BT / 64;        // 16 x 16 tiles of a wave
+  constexpr int kWOps = BN / 128, kXOps = BT / 64;  // DMA instructions of a wave, 8 rows each: a group's rows; the tokens
+  struct Tokens {
+    uint8_t x[BT * 128];
     uint32_t s[BT];
   };
-  __shared__ __attribute__((aligned(1024))) Stage s0;
-  __shared__ __attribute__((aligned(1024))) Stage s1;
+  __shared__ __attribute__((aligned(1024))) Tokens x0;
+  __shared__ __attribute__((aligned(1024))) Tokens x1;
+  __shared__ __attribute__((aligned(1024))) uint8_t wa0[BN * 64];
+  __shared__ __attribute__((aligned(1024))) uint8_t wa1[BN * 64];
+  __shared__ __attribute__((aligned(1024))) uint8_t wb0[BN * 64];
+  __shared__ __attribute__((aligned(1024))) uint8_t wb1[BN * 64];
+  __shared__ uint32_t w_scale[2][MOE_MAX_DIM / 128];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int group = wave >> 2, wt = wave & 3;
   const int r = lane & 15, g = lane >> 4;
 
   // Blocks are dealt to the 8 XCDs in turn: each XCD gets a run of consecutive
-  // units, and a run covers eight token tiles before it goes to the next rows
+  // units, and a run covers kBand token tiles before it goes to the next rows
   // of W, so that the blocks an XCD runs at once share both operands in its L2.
+  constexpr int kBand = 4;
   const int total = a.n_tiles * a.t_tiles, per = (total + 7) >> 3;
   const int unit = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
   if ((blockIdx.x >> 3) >= per || unit >= total) return;
-  const int band = unit / (8 * a.n_tiles), in_band = unit - band * 8 * a.n_tiles;
-  const int wide = min(8, a.t_tiles - 8 * band);
-  const int t0 = (8 * band + in_band % wide) * BT, n0 = (in_band / wide) * BN;
-  const int wn = wave % WN, wt = wave / WN;
+  const int band = unit / (kBand * a.n_tiles), in_band = unit - band * kBand * a.n_tiles;
+  const int wide = min(kBand, a.t_tiles - kBand * band);
+  const int t0 = __builtin_amdgcn_readfirstlane((kBand * band + in_band % wide) * BT);
+  const int n0 = __builtin_amdgcn_readfirstlane((in_band / wide) * BN);
 
-  const int Kp = 128 * a.kb;
-  int64_t woff[kWOps], xoff[kXOps];
-  int wk[kWOps];
-#pragma unroll
-  for (int i = 0; i < kWOps; ++i) {
-    const int row = 8 * (kWaves * i + wave) + (lane >> 3);
-    woff[i] = static_cast<int64_t>(min(n0 + row, a.N - 1)) * a.K;
-    wk[i] = 16 * slot(row, lane & 7);
+  // W's scales of the two groups' rows
+  for (int i = threadIdx.x; i < 2 * a.kb; i += 512) {
+    const int h = i >= a.kb, b = i - (h ? a.kb : 0);
+    w_scale[h][b] = weight_scale<F32>(a.w_scale, static_cast<int64_t>(min(n0 + h * (BN / 2), a.N - 1) >> 7) * a.kb + b);
   }
+
+  // Sources: one 32-bit lane offset per operand from the part's first row (the
+  // instructions of a wave are 64 rows apart).  Rows past the end of W or x lie
+  // past the end of the resource, which reads as zeros; they are not stored.
+  // So do the blocks past the last one, which the loop asks for: their resource
+  // is empty, and no memory is read.
+  const int w_bytes[2] = {__builtin_amdgcn_readfirstlane(min(BN / 2, a.N - n0) * a.K),
+                          __builtin_amdgcn_readfirstlane(max(min(BN / 2, a.N - n0 - BN / 2), 0) * a.K)};
+  const int x_rows = __builtin_amdgcn_readfirstlane(min(BT, a.T - t0));
+  const int row0 = 8 * wave + (lane >> 3);
+  auto issue_w = [&](int h, uint8_t* to, int b) __attribute__((always_inline)) {
+    int row = row0;
+    asm volatile("" : "+v"(row));  // derived offsets are not kept in registers from step to step
+    const __amdgpu_buffer_rsrc_t src =
+        raw_buffer(a.w + static_cast<int64_t>(n0 + h * (BN / 2)) * a.K, b < a.kb ? w_bytes[h] : 0);
+    const int k = row * a.K + min(128 * b + 16 * slot(row, lane & 7), a.K - 16);
 #pragma unroll
-  for (int i = 0; i < kXOps; ++i) {
-    const int row = 8 * (kWaves * i + wave) + (lane >> 3);
-    xoff[i] = static_cast<int64_t>(min(t0 + row, a.T - 1)) * Kp + 16 * slot(row, lane & 7);
-  }
-  const int srow = min(t0 + 64 * wave + lane, a.T - 1);
-  auto issue = [&](Stage& to, int b) {
-#pragma unroll
-    for (int i = 0; i < kWOps; ++i)
-      dma16(a.w + woff[i] + min(128 * b + wk[i], a.K - 16), &to.w[1024 * (kWaves * i + wave)]);
+    for (int i = 0; i < kWOps; ++i) dma16(src, k + 64 * i * a.K, 0, to + 1024 * (8 * i + wave));
+  };
+  const int spart = wave % (BT / 64);
+  auto issue_x = [&](Tokens& to, int b) __attribute__((always_inline)) {
+    int row = row0;
+    asm volatile("" : "+v"(row));
+    const int64_t first = static_cast<int64_t>(b) * a.T + t0;
+    const int rows = b < a.kb ? x_rows : 0;
+    const __amdgpu_buffer_rsrc_t src = raw_buffer(a.codes + 128 * first, 128 * rows);
 #pragma unroll
     for (int i = 0; i < kXOps; ++i)
-      dma16(a.codes + xoff[i] + 128 * b, &to.x[1024 * (kWaves * i + wave)]);
-    if (wave < BT / 64) dma4(a.scales + static_cast<int64_t>(b) * a.T + srow, &to.s[64 * wave]);
+      dma16(src, 128 * row + 16 * slot(row, lane & 7) + 8192 * i, 0, &to.x[1024 * (8 * i + wave)]);
+    dma4(raw_buffer(a.scales + first, 4 * rows), 4 * (64 * spart + lane), &to.s[64 * spart]);
   };
 
-  const int64_t wrow = static_cast<int64_t>(min(n0 + wn * (BN / WN), a.N - 1) >> 7) * a.kb;
   f32x4 acc[kN][kT];
 #pragma unroll
   for (int i = 0; i < kN; ++i)
 #pragma unroll
     for (int j = 0; j < kT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  uint32_t sw_next = weight_scale<F32>(a.w_scale, wrow);
-  auto step = [&](const Stage& now, Stage& next, int b) {
-    wait_vmcnt<0>();
-    stage_barrier();
-    const uint32_t sw = sw_next;
-    if (b + 1 < a.kb) {
-      issue(next, b + 1);
-      sw_next = weight_scale<F32>(a.w_scale, wrow + b + 1);
-    }
+  i32x8 wf[kN], xf[kT];
+  uint32_t sx[kT], sw;
+  const int operand = 128 * r + 16 * slot(r, g);  // chunk 4 + g is at ^ 64
+  auto read = [&](const Tokens& x, const uint8_t* w, int b) __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
-    i32x8 xf[kT];
-    uint32_t sx[kT];
-    float f[kT];
+    int c = operand;
+    asm volatile("" : "+v"(c));
+    const uint8_t* xp = &x.x[128 * (BT / 4) * wt];
 #pragma unroll
     for (int j = 0; j < kT; ++j) {
-      const int row = (BT / WT) * wt + 16 * j + r;
-      xf[j] = join(ld16(&now.x[128 * row + 16 * slot(row, g)]), ld16(&now.x[128 * row + 16 * slot(row, 4 + g)]));
-      sx[j] = now.s[row];
-      f[j] = F32 ? __uint_as_float(sx[j]) * __uint_as_float(sw) : 0.f;
+      xf[j] = join(ld16(xp + 2048 * j + c), ld16(xp + 2048 * j + (c ^ 64)));
+      sx[j] = x.s[(BT / 4) * wt + 16 * j + (c >> 7)];
     }
+    sw = w_scale[group][b];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int row = (BN / WN) * wn + 16 * i + r;
-      const i32x8 wf = join(ld16(&now.w[128 * row + 16 * slot(row, g)]), ld16(&now.w[128 * row + 16 * slot(row, 4 + g)]));
-#pragma unroll
-      for (int j = 0; j < kT; ++j)
-        block_mfma<F32>(wf, xf[j], acc[i][j], static_cast<int>(sw), static_cast<int>(sx[j]), f[j]);
-    }
+    for (int i = 0; i < kN; ++i) wf[i] = join(ld16(w + 2048 * i + c), ld16(w + 2048 * i + (c ^ 64)));
+    __builtin_amdgcn_sched_barrier(0);
   };
-  issue(s0, 0);
-  for (int b = 0; b < a.kb; b += 2) {
-    step(s0, s1, b);
-    if (b + 1 < a.kb) step(s1, s0, b + 1);
+  auto multiply = [&]() __attribute__((always_inline)) {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+    float f[kT];
+    if (F32) {
+#pragma unroll
+      for (int j = 0; j < kT; ++j) f[j] = __uint_as_float(sx[j]) * __uint_as_float(sw);
+    }
+    f32x4 p[2];
+#pragma unroll
+    for (int u = 0; u < kN * kT; ++u) {
+      const int i = u / kT, j = u % kT;
+      if (F32) {
+        // one product, and beside it the sum of the product before
+        const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+        p[u & 1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[i], xf[j], z, 0, 0, 0, 127, 0, 127);
+        if (u > 0) {
+          const int i1 = (u - 1) / kT, j1 = (u - 1) % kT;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i1][j1][e] = __builtin_fmaf(f[j1], p[(u - 1) & 1][e], acc[i1][j1][e]);
+        }
+      } else {
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[i], xf[j], acc[i][j], 0, 0, 0,
+                                                                     static_cast<int>(sw), 0, static_cast<int>(sx[j]));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (F32) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        acc[kN - 1][kT - 1][e] = __builtin_fmaf(f[kT - 1], p[(kN * kT - 1) & 1][e], acc[kN - 1][kT - 1][e]);
+    }
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // The end of an even phase: group 1's rows of the block have arrived; rows of
+  // group 0, tokens and rows of group 1 were issued since.
+  auto end_even = [&]() __attribute__((always_inline)) {
+    wait_vmcnt<2 * kWOps + kXOps + 1>();
+    stage_barrier();
+  };
+  // The end of an odd phase: the next block's tokens and rows of group 0 have
+  // arrived; rows of group 1 and of group 0 were issued since.
+  auto end_odd = [&]() __attribute__((always_inline)) {
+    wait_vmcnt<2 * kWOps>();
+    stage_barrier();
+  };
+
+  issue_w(0, wa0, 0);
+  issue_x(x0, 0);
+  issue_w(1, wb0, 0);
+  issue_w(0, wa1, 1);
+  wait_vmcnt<0>();
+  stage_barrier();
+  int b = 0;
+  if (group == 0) {
+    auto step = [&](const Tokens& x, uint8_t* wa, Tokens& xn, uint8_t* wbn) __attribute__((always_inline)) {
+      issue_x(xn, b + 1);
+      issue_w(1, wbn, b + 1);
+      read(x, wa, b);
+      end_even();
+      issue_w(0, wa, b + 2);
+      multiply();
+      end_odd();
+      ++b;
+    };
+    while (b + 1 < a.kb) {
+      step(x0, wa0, x1, wb1);
+      step(x1, wa1, x0, wb0);
+    }
+    if (b < a.kb) step(x0, wa0, x1, wb1);
+  } else {
+    auto step = [&](const Tokens& x, const uint8_t* wb, uint8_t* wa, Tokens& xn,
+                    uint8_t* wbn) __attribute__((always_inline)) {
+      issue_x(xn, b + 1);
+      issue_w(1, wbn, b + 1);
+      if (b > 0) multiply();
+      end_even();
+      issue_w(0, wa, b + 2);
+      read(x, wb, b);
+      end_odd();
+      ++b;
+    };
+    while (b + 1 < a.kb) {
+      step(x0, wb0, wa0, x1, wb1);
+      step(x1, wb1, wa1, x0, wb0);
+    }
+    if (b < a.kb) step(x0, wb0, wa0, x1, wb1);
+    multiply();
   }
+  wait_vmcnt<0>();  // no DMA is left for the LDS of the next block
 
 #pragma unroll
   for (int j = 0; j < kT; ++j) {
-    const int t = t0 + (BT / WT) * wt + 16 * j + r;
+    const int t = t0 + (BT / 4) * wt + 16 * j + r;
     if (t >= a.T) continue;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int n = n0 + (BN / WN) * wn + 16 * i + 4 * g;
+      const int n = n0 + group * (BN / 2) + 16 * i + 4 * g;
       store4(a.y, a.y_stride, t, n, a.N, a.wide, acc[i][j]);
     }
   }
@@ -375,10 +486,10 @@ void launch(LinearArgs& a, hipStream_t s) {
   };
   if (ceil_div(a.N, 256) * ceil_div(a.T, 256) >= 256) {
     const unsigned grid = tiles(256, 256);
-    fp8_tile_kernel<256, 256, 2, 4, F32><<<grid, 512, 0, s>>>(a);
+    fp8_tile_kernel<256, 256, F32><<<grid, 512, 0, s>>>(a);
   } else {
     const unsigned grid = tiles(128, 128);
-    fp8_tile_kernel<128, 128, 2, 2, F32><<<grid, 256, 0, s>>>(a);
+    fp8_tile_kernel<128, 128, F32><<<grid, 512, 0, s>>>(a);
   }
 }
 

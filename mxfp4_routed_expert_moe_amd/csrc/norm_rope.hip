@@ -5,10 +5,11 @@
 // power of two), eight consecutive elements each: one 16-byte load, a sum of
 // squares over the group by lane exchanges, one 16-byte store.  A rotated pair
 // lies either inside a lane (interleaved) or in two lanes rot_dim / 16 apart,
-// which exchange their inputs as stored (four words rather than eight floats: the
-// partner's norm factor is the same, and its weights are loaded beside the own
-// ones).  A block keeps to one token, so its cosines and sines are loaded
-// once and serve all of the heads that a group takes in turn.
+// which exchange their inputs as stored (four words rather than eight floats).
+// Norm weight, cosine and sine do not depend on the head, so with a lane's own
+// inputs x and its partners' y an output is f (x A + y B), f = 1 / sqrt(mean(x^2) +
+// eps), and A and B are built once for the HP heads of one token that a group
+// takes: A = w c, B = -+ w' s.
 #include <math.h>
 
 #include "../../include/moe_attention.h"
@@ -22,6 +23,7 @@ struct NormArgs {
   moe_heads q, k, q_out, k_out;
   const float *qw, *kw, *cs;
   const int32_t* pos;
+  unsigned T, chunks;  // chunks of heads per token
   int q_heads, heads;  // heads = q_heads + k_heads
   int D, P, R, off;
   float eps, inv_d;
@@ -35,28 +37,58 @@ __device__ __forceinline__ void unpack8(u32x4 w, float (&f)[8]) {
   }
 }
 
+// Eight values, or four of them twice each.
+template <bool TWICE>
 __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p);
+  if (TWICE) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
+    for (int i = 0; i < 8; ++i) f[i] = a[i / 2];
+  } else {
+    const f32x4 b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
+  }
 }
 
-// grid (T, chunks of 256 / L * HP heads); group g of a block takes heads g,
-// g + 256 / L, ... of its chunk.
+// The sum over a group of L lanes, in every lane of it.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 15, 15, true));
+}
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+  v = dpp_add<0xb1>(v);   // quad_perm 1 0 3 2
+  v = dpp_add<0x4e>(v);   // quad_perm 2 3 0 1
+  v = dpp_add<0x141>(v);  // mirror within 8
+  if (L >= 16) v = dpp_add<0x140>(v);  // mirror within 16
+  if (L >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if (L >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return v;
+}
+
+// Unit u = (token, chunk of HP heads) per group of L lanes.
 template <int L, int HP, bool INTER>
 __global__ __launch_bounds__(256) void norm_rope_kernel(NormArgs a) {
-  constexpr int kGroups = 256 / L;
-  const int t = blockIdx.x;
-  const int l = threadIdx.x % L, g = threadIdx.x / L;
-  const int e0 = 8 * l;
-  const bool in = e0 < a.D;
-  const int h0 = blockIdx.y * (kGroups * HP) + g;
+  const unsigned u = blockIdx.x * (256 / L) + threadIdx.x / L;
+  const unsigned token = u / a.chunks;
+  const bool live = token < a.T;
+  const unsigned t = live ? token : 0;
+  const int h0 = static_cast<int>(u - token * a.chunks) * HP;
+  const int l = threadIdx.x % L, e0 = 8 * l;
+  const bool in = live && e0 < a.D;
 
   // all the loads of the heads first
   u32x4 raw[HP];
 #pragma unroll
   for (int i = 0; i < HP; ++i) {
-    const int h = h0 + i * kGroups;
+    const int h = h0 + i;
     raw[i] = u32x4{0, 0, 0, 0};
     if (in && h < a.heads) {
       const bool is_q = h < a.q_heads;
@@ -65,113 +97,116 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormArgs a) {
     }
   }
 
-  const int r0 = e0 - a.off;                          // place in the rotated range
+  const int r0 = e0 - a.off;  // place in the rotated range
   const bool rot = in && r0 >= 0 && r0 < a.R;
   const int half = a.R >> 1;
-  const bool first = r0 < half;                       // of the two halves
-  const int mate = INTER ? l : l + (first ? half : -half) / 8;  // lane in the group that holds the partners
+  const bool first = r0 < half;  // of the two halves
+  const int step = INTER ? 0 : rot ? (first ? half : -half) : 0;  // to the partners
+  const int mate = 4 * (static_cast<int>(threadIdx.x & 63) + step / 8);
+  // the angles of the lane's elements: cosine, and sine with the sign its product takes
   float c[8], s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
   if (rot) {
     const int p = a.pos[t];
-    if (p < 0 || p >= a.P) {
+    const bool ok = p >= 0 && p < a.P;
+    const float* row = a.cs + static_cast<int64_t>(ok ? p : 0) * a.R + (INTER ? r0 / 2 : first ? r0 : r0 - half);
+    if (a.P > 0) {
+      load8<INTER>(row, c);
+      load8<INTER>(row + half, s);
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = s[i] = __builtin_nanf("");
-    } else {
-      const float* row = a.cs + static_cast<int64_t>(p) * a.R;
-      if (INTER) {
-        const f32x4 cv = *reinterpret_cast<const f32x4*>(row + r0 / 2), sv = *reinterpret_cast<const f32x4*>(row + half + r0 / 2);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = cv[i], s[i] = sv[i];
-      } else {
-        load8(row + (first ? r0 : r0 - half), c);
-        load8(row + half + (first ? r0 : r0 - half), s);
-        if (first) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s[i] = -s[i];
-        }
-      }
+    for (int i = 0; i < 8; ++i) {
+      if (INTER ? i % 2 == 0 : first) s[i] = -s[i];
+      if (!ok) c[i] = s[i] = __builtin_nanf("");
     }
   }
-  const int mate_e0 = rot ? 8 * mate : (in ? e0 : 0);
 
+  float A[8], B[8];
 #pragma unroll
   for (int i = 0; i < HP; ++i) {
-    const int h = h0 + i * kGroups;
-    if (blockIdx.y * (kGroups * HP) + i * kGroups >= a.heads) break;  // the same for the whole block
+    const int h = h0 + i;
+    if (HP > 1 && !__any(h < a.heads)) break;
     const bool is_q = h < a.q_heads;
-    float x[8];
+    if (i == 0 || h == a.q_heads) {
+      const float* wp = is_q ? a.qw : a.kw;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) A[j] = B[j] = 1.f;
+      if (wp && in) {
+        load8<false>(wp + e0, A);
+        load8<false>(wp + e0 + step, B);
+      }
+      if (INTER) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float v = B[j];
+          B[j] = B[j + 1], B[j + 1] = v;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) A[j] *= c[j], B[j] *= s[j];
+    }
+    float x[8], y[8];
     unpack8(raw[i], x);
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(x[j], x[j], sum);
+    const float f = rsqrtf(__builtin_fmaf(group_sum<L>(sum), a.inv_d, a.eps));
+    if (INTER) {
 #pragma unroll
-    for (int d = 1; d < L; d <<= 1) sum += __shfl_xor(sum, d, L);
-    const float f = 1.f / sqrtf(__builtin_fmaf(sum, a.inv_d, a.eps));
-    const float* wp = is_q ? a.qw : a.kw;
-    float w[8];
+      for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
+    } else {
+      u32x4 other;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 1.f;
-    if (wp && in) load8(wp + e0, w);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = x[j] * f * w[j];
-    if (a.R) {
-      if (INTER) {
-        if (rot) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float u = x[2 * j], v = x[2 * j + 1];
-            x[2 * j] = u * c[j] - v * s[j];
-            x[2 * j + 1] = v * c[j] + u * s[j];
-          }
-        }
-      } else {
-        u32x4 other;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) other[j] = __shfl(raw[i][j], rot ? mate : l, L);
-        float y[8];
-        unpack8(other, y);
-        if (wp) load8(wp + mate_e0, w);
-        if (rot) {
-          // s is -sin in the first half, sin in the second
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = x[j] * c[j] + y[j] * f * w[j] * s[j];
-        }
-      }
+      for (int j = 0; j < 4; ++j)
+        other[j] = static_cast<unsigned>(__builtin_amdgcn_ds_bpermute(mate, static_cast<int>(raw[i][j])));
+      unpack8(other, y);
     }
     if (in && h < a.heads) {
       const moe_heads& o = is_q ? a.q_out : a.k_out;
       u32x4 v;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] = float_to_bf16_bits(x[2 * j]) | static_cast<uint32_t>(float_to_bf16_bits(x[2 * j + 1])) << 16;
-      *reinterpret_cast<u32x4*>(o.base + t * o.row_stride + (is_q ? h : h - a.q_heads) * o.head_stride + e0) = v;
+      for (int j = 0; j < 4; ++j) {
+        // an element that is not rotated has B = 0 and its own input as y
+        const float p0 = f * __builtin_fmaf(x[2 * j], A[2 * j], y[2 * j] * B[2 * j]);
+        const float p1 = f * __builtin_fmaf(x[2 * j + 1], A[2 * j + 1], y[2 * j + 1] * B[2 * j + 1]);
+        v[j] = float_to_bf16_bits(p0) | static_cast<uint32_t>(float_to_bf16_bits(p1)) << 16;
+      }
+      u32x4* to = reinterpret_cast<u32x4*>(o.base + t * o.row_stride + (is_q ? h : h - a.q_heads) * o.head_stride + e0);
+      if (HP > 1)
+        __builtin_nontemporal_store(v, to);
+      else
+        *to = v;
     }
   }
 }
 
+// Lanes of work from which a group takes four heads: below, one head each
+// spreads the work over more of the card.
+constexpr int64_t kManyLanes = int64_t{1} << 18;
+
 template <int L, bool INTER>
-void launch(const NormArgs& a, int T, hipStream_t s) {
-  constexpr int kGroups = 256 / L;
+void launch(NormArgs a, hipStream_t s) {
   constexpr int kMany = 4;
-  // few tokens: one head per group, so that the heads spread over the card
-  if (a.heads <= kGroups || static_cast<int64_t>(T) * a.heads <= 1024 * kGroups)
-    norm_rope_kernel<L, 1, INTER><<<dim3(T, (a.heads + kGroups - 1) / kGroups), 256, 0, s>>>(a);
+  const bool many = static_cast<int64_t>(a.T) * a.heads * L >= kManyLanes;
+  a.chunks = many ? (a.heads + kMany - 1) / kMany : a.heads;
+  const unsigned blocks = (static_cast<unsigned>(a.T) * a.chunks + 256 / L - 1) / (256 / L);
+  if (many)
+    norm_rope_kernel<L, kMany, INTER><<<blocks, 256, 0, s>>>(a);
   else
-    norm_rope_kernel<L, kMany, INTER><<<dim3(T, (a.heads + kGroups * kMany - 1) / (kGroups * kMany)), 256, 0, s>>>(a);
+    norm_rope_kernel<L, 1, INTER><<<blocks, 256, 0, s>>>(a);
 }
 
 template <bool INTER>
-void launch_for(const NormArgs& a, int T, hipStream_t s) {
+void launch_for(const NormArgs& a, hipStream_t s) {
   if (a.D <= 64)
-    launch<8, INTER>(a, T, s);
+    launch<8, INTER>(a, s);
   else if (a.D <= 128)
-    launch<16, INTER>(a, T, s);
+    launch<16, INTER>(a, s);
   else if (a.D <= 256)
-    launch<32, INTER>(a, T, s);
+    launch<32, INTER>(a, s);
   else
-    launch<64, INTER>(a, T, s);
+    launch<64, INTER>(a, s);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -207,13 +242,14 @@ extern "C" int moe_qk_norm_rope(const moe_heads* q, int32_t q_heads, const moe_h
   a.q = *q, a.q_out = *q_out;
   a.k = k_heads ? *k : moe_heads{}, a.k_out = k_heads ? *k_out : moe_heads{};
   a.qw = q_weight, a.kw = k_weight, a.cs = cos_sin, a.pos = positions;
+  a.T = static_cast<unsigned>(T), a.chunks = 0;
   a.q_heads = q_heads, a.heads = q_heads + k_heads;
   a.D = head_dim, a.P = n_positions, a.R = rot_dim, a.off = rot_offset;
   a.eps = eps, a.inv_d = 1.f / static_cast<float>(head_dim);
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (interleaved)
-    moe::launch_for<true>(a, T, s);
+    moe::launch_for<true>(a, s);
   else
-    moe::launch_for<false>(a, T, s);
+    moe::launch_for<false>(a, s);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
 }
