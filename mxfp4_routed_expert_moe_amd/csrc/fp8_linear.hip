@@ -143,92 +143,116 @@ struct LinearArgs {
 };
 
 // ---------------------------------------------------------------- few tokens
-// A block holds 16 rows of W and 16 * MT tokens; its NW waves take the blocks of
+// A block holds 16 NI rows of W and 16 MT tokens; its NW waves take the blocks of
 // K in turn, straight from memory, and meet in LDS.  W is read once per token
-// block: the kernel streams it.  QUANT: x is quantised on the way in (each of
-// the four lanes of a token holds 32 columns of the block).
+// block: the kernel streams it.  QUANT: the block quantises x itself, into LDS,
+// while its first loads of W are on their way.
 constexpr int kNW = 8;
+constexpr int kFusedBytes = 16 << 10;  // codes of x that the block quantises itself
 
-template <int MT, bool F32, bool QUANT>
+template <int MT, int NI, bool F32, bool QUANT>
 __global__ __launch_bounds__(64 * kNW) void fp8_few_kernel(LinearArgs a) {
-  constexpr int kU = MT == 1 ? 4 : 2;  // blocks of K in flight per wave
-  __shared__ f32x4 part[kNW][MT][64];
+  static_assert(MT * NI <= kNW, "a wave per tile at the end");
+  constexpr int kU = MT * NI <= 4 ? 4 : 2;  // blocks of K in flight per wave
+  __shared__ f32x4 part[kNW][MT * NI][64];
+  __shared__ __attribute__((aligned(16))) uint8_t q_codes[QUANT ? kFusedBytes : 16];
+  __shared__ uint32_t q_scales[QUANT ? kFusedBytes / 128 : 1];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r = lane & 15, g = lane >> 4;
-  const int n0 = 16 * blockIdx.x, t0 = 16 * MT * blockIdx.y;
-  const uint8_t* wp = a.w + static_cast<int64_t>(min(n0 + r, a.N - 1)) * a.K;
-  const int64_t srow = static_cast<int64_t>(n0 >> 7) * a.kb;
+  const int n0 = 16 * NI * blockIdx.x, t0 = 16 * MT * blockIdx.y;
+  const uint8_t* wp[NI];
+  int64_t srow[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    wp[i] = a.w + static_cast<int64_t>(min(n0 + 16 * i + r, a.N - 1)) * a.K;
+    srow[i] = static_cast<int64_t>(min(n0 + 16 * i, a.N - 1) >> 7) * a.kb;
+  }
   const int last = a.K - 16;
 
-  f32x4 acc[MT];
+  f32x4 acc[NI][MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[i][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  u32x4 wv[kU][NI][2];
+  uint32_t sw[kU][NI];
+  auto load_w = [&](int b0) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int b = min(b0 + u * kNW, a.kb - 1), k = 128 * b + 32 * g;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        wv[u][i][0] = ld16(wp[i] + min(k, last));
+        wv[u][i][1] = ld16(wp[i] + min(k + 16, last));
+        sw[u][i] = weight_scale<F32>(a.w_scale, srow[i] + b);
+      }
+    }
+  };
+  load_w(wave);
+  if (QUANT) {
+    __builtin_amdgcn_sched_barrier(0);
+    // 16 lanes per token and block of K, 8 values each
+    const int cols = a.kb * 16;
+    for (int u = threadIdx.x; u < a.T * cols; u += 64 * kNW) {
+      const int t = u / cols, c = u - t * cols;
+      u32x4 w = {0, 0, 0, 0};
+      if (8 * c < a.K) w = ld16(a.x + t * a.x_stride + 8 * c);
+      float m = max_abs(w, 0.f), inv;
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 16));
+      const uint32_t s = block_scale<F32>(m, inv);
+      *reinterpret_cast<u32x2*>(&q_codes[8 * u]) = u32x2{codes4(w[0], w[1], inv), codes4(w[2], w[3], inv)};
+      if ((u & 15) == 0) q_scales[u >> 4] = s;
+    }
+    stage_barrier();  // leaves the loads of W in flight
+  }
 
   for (int b0 = wave; b0 < a.kb; b0 += kNW * kU) {
-    u32x4 wv[kU][2], xv[kU][MT][QUANT ? 4 : 2];
-    uint32_t sw[kU], sx[kU][MT];
+    u32x4 xv[kU][MT][2];
+    uint32_t sx[kU][MT];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int b = min(b0 + u * kNW, a.kb - 1);
-      const int k = 128 * b + 32 * g;
-      wv[u][0] = ld16(wp + min(k, last));
-      wv[u][1] = ld16(wp + min(k + 16, last));
-      sw[u] = weight_scale<F32>(a.w_scale, srow + b);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const int t = min(t0 + 16 * m + r, a.T - 1);
-        if (QUANT) {
-          const uint16_t* p = a.x + t * a.x_stride + k;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            xv[u][m][i] = u32x4{0, 0, 0, 0};
-            if (k + 8 * i < a.K && t0 + 16 * m + r < a.T) xv[u][m][i] = ld16(p + 8 * i);
-          }
-        } else {
-          const uint8_t* p = a.codes + (static_cast<int64_t>(b) * a.T + t) * 128 + 32 * g;
-          xv[u][m][0] = ld16(p);
-          xv[u][m][1] = ld16(p + 16);
-          sx[u][m] = a.scales[static_cast<int64_t>(b) * a.T + t];
-        }
+        const uint8_t* p = QUANT ? &q_codes[128 * (t * a.kb + b) + 32 * g]
+                                 : a.codes + (static_cast<int64_t>(b) * a.T + t) * 128 + 32 * g;
+        xv[u][m][0] = ld16(p);
+        xv[u][m][1] = ld16(p + 16);
+        sx[u][m] = QUANT ? q_scales[t * a.kb + b] : a.scales[static_cast<int64_t>(b) * a.T + t];
       }
     }
+    __builtin_amdgcn_sched_barrier(0);  // all of them are on their way before the first is used
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       if (b0 + u * kNW >= a.kb) break;
-      const i32x8 wf = join(wv[u][0], wv[u][1]);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        i32x8 xf;
-        if (QUANT) {
-          float top = 0.f, inv;
+      for (int i = 0; i < NI; ++i) {
+        const i32x8 wf = join(wv[u][i][0], wv[u][i][1]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) top = max_abs(xv[u][m][i], top);
-          top = fmaxf(top, __shfl_xor(top, 16, 64));
-          top = fmaxf(top, __shfl_xor(top, 32, 64));
-          sx[u][m] = block_scale<F32>(top, inv);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            xf[2 * i] = static_cast<int>(codes4(xv[u][m][i][0], xv[u][m][i][1], inv));
-            xf[2 * i + 1] = static_cast<int>(codes4(xv[u][m][i][2], xv[u][m][i][3], inv));
-          }
-        } else {
-          xf = join(xv[u][m][0], xv[u][m][1]);
+        for (int m = 0; m < MT; ++m) {
+          const float f = F32 ? __uint_as_float(sw[u][i]) * __uint_as_float(sx[u][m]) : 0.f;
+          block_mfma<F32>(wf, join(xv[u][m][0], xv[u][m][1]), acc[i][m], static_cast<int>(sw[u][i]),
+                          static_cast<int>(sx[u][m]), f);
         }
-        const float f = F32 ? __uint_as_float(sw[u]) * __uint_as_float(sx[u][m]) : 0.f;
-        block_mfma<F32>(wf, xf, acc[m], static_cast<int>(sw[u]), static_cast<int>(sx[u][m]), f);
       }
     }
+    if (b0 + kNW * kU < a.kb) load_w(b0 + kNW * kU);
   }
 
 #pragma unroll
-  for (int m = 0; m < MT; ++m) part[wave][m][lane] = acc[m];
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) part[wave][i * MT + m][lane] = acc[i][m];
   __syncthreads();
-  if (wave >= MT) return;
+  if (wave >= MT * NI) return;
   f32x4 v = part[0][wave][lane];
 #pragma unroll
   for (int i = 1; i < kNW; ++i) v += part[i][wave][lane];
-  const int t = t0 + 16 * wave + r;
-  if (t < a.T) store4(a.y, a.y_stride, t, n0 + 4 * g, a.N, a.wide, v);
+  const int t = t0 + 16 * (wave % MT) + r;
+  if (t < a.T) store4(a.y, a.y_stride, t, n0 + 16 * (wave / MT) + 4 * g, a.N, a.wide, v);
 }
 
 // ---------------------------------------------------------------- many tokens
@@ -458,25 +482,30 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t align256(size_t v) { return (v + 255) & ~size_t{255}; }
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-constexpr int kFusedTokens = 16;  // x is quantised inside the few-token kernel up to here
-
 bool shape_ok(int32_t T, int32_t N, int32_t K) {
   return T >= 0 && T <= MOE_MAX_TOKENS && N > 0 && N <= MOE_MAX_DIM && K > 0 && K <= MOE_MAX_DIM && K % 16 == 0;
 }
 
+constexpr int64_t kFillCard = 192;  // blocks from which larger ones, that read x less often, are worth it
+
 template <bool F32>
 void launch(LinearArgs& a, hipStream_t s) {
-  if (a.T <= kFusedTokens) {
-    fp8_few_kernel<1, F32, true><<<dim3(ceil_div(a.N, 16), 1), 64 * kNW, 0, s>>>(a);
+  if (a.T <= 16 && a.T * a.kb * 128 <= kFusedBytes) {
+    fp8_few_kernel<1, 1, F32, true><<<dim3(ceil_div(a.N, 16), 1), 64 * kNW, 0, s>>>(a);
     return;
   }
   fp8_quant_kernel<F32><<<static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.T) * a.kb, 16)), 256, 0, s>>>(
       a.x, a.x_stride, a.T, a.K, a.kb, const_cast<uint8_t*>(a.codes), const_cast<uint32_t*>(a.scales));
   if (a.T <= 64 || ceil_div(a.N, 128) * ceil_div(a.T, 128) < 128) {
-    if (a.T <= 32)
-      fp8_few_kernel<2, F32, false><<<dim3(ceil_div(a.N, 16), ceil_div(a.T, 32)), 64 * kNW, 0, s>>>(a);
+    const unsigned t64 = static_cast<unsigned>(ceil_div(a.T, 64));
+    if (a.T <= 16)
+      fp8_few_kernel<1, 1, F32, false><<<dim3(ceil_div(a.N, 16), 1), 64 * kNW, 0, s>>>(a);
+    else if (a.T <= 32)
+      fp8_few_kernel<2, 1, F32, false><<<dim3(ceil_div(a.N, 16), 1), 64 * kNW, 0, s>>>(a);
+    else if (ceil_div(a.N, 32) * t64 < kFillCard)
+      fp8_few_kernel<4, 1, F32, false><<<dim3(ceil_div(a.N, 16), t64), 64 * kNW, 0, s>>>(a);
     else
-      fp8_few_kernel<4, F32, false><<<dim3(ceil_div(a.N, 16), ceil_div(a.T, 64)), 64 * kNW, 0, s>>>(a);
+      fp8_few_kernel<4, 2, F32, false><<<dim3(ceil_div(a.N, 32), t64), 64 * kNW, 0, s>>>(a);
     return;
   }
   auto tiles = [&](int bn, int bt) {
