@@ -486,7 +486,18 @@ bool shape_ok(int32_t T, int32_t N, int32_t K) {
   return T >= 0 && T <= MOE_MAX_TOKENS && N > 0 && N <= MOE_MAX_DIM && K > 0 && K <= MOE_MAX_DIM && K % 16 == 0;
 }
 
-constexpr int64_t kFillCard = 192;  // blocks from which larger ones, that read x less often, are worth it
+// Which kernel, by how many blocks there are to fill the card (microseconds at K =
+// 4096, E8M0 scales, quantisation included):
+//   few-token kernel against 128 x 128 tiles, by the number of those tiles: 32
+//   tiles (T = 512, N = 1024) 17.5 against 24.6, 64 tiles (T = 256, N = 4096) 30.0
+//   against 29.0, 96 tiles (T = 256, N = 6144) 44.4 against 31.8;
+//   128 x 128 against 256 x 256 tiles, by the number of the latter: 96 tiles (T =
+//   1024, N = 6144) 45.6 against 59.4, 128 tiles (T = 2048, N = 4096) 50.9 against
+//   61.6, 192 tiles (T = 2048, N = 6144) 75.3 against 66.2;
+//   one or two row tiles of W per block of the few-token kernel, by the blocks with
+//   two: 128 blocks (T = 64, N = 4096) 15.6 against 16.8, 252 blocks (T = 509,
+//   N = 1000, K = 2064) 14.5 against 10.2.
+constexpr int64_t kTiles128 = 64, kTiles256 = 192, kFillCard = 192;
 
 template <bool F32>
 void launch(LinearArgs& a, hipStream_t s) {
@@ -496,7 +507,7 @@ void launch(LinearArgs& a, hipStream_t s) {
   }
   fp8_quant_kernel<F32><<<static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.T) * a.kb, 16)), 256, 0, s>>>(
       a.x, a.x_stride, a.T, a.K, a.kb, const_cast<uint8_t*>(a.codes), const_cast<uint32_t*>(a.scales));
-  if (a.T <= 64 || ceil_div(a.N, 128) * ceil_div(a.T, 128) < 128) {
+  if (a.T <= 64 || ceil_div(a.N, 128) * ceil_div(a.T, 128) < kTiles128) {
     const unsigned t64 = static_cast<unsigned>(ceil_div(a.T, 64));
     if (a.T <= 16)
       fp8_few_kernel<1, 1, F32, false><<<dim3(ceil_div(a.N, 16), 1), 64 * kNW, 0, s>>>(a);
@@ -513,7 +524,7 @@ void launch(LinearArgs& a, hipStream_t s) {
     a.t_tiles = static_cast<int>(ceil_div(a.T, bt));
     return static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.n_tiles) * a.t_tiles, 8) * 8);
   };
-  if (ceil_div(a.N, 256) * ceil_div(a.T, 256) >= 256) {
+  if (ceil_div(a.N, 256) * ceil_div(a.T, 256) >= kTiles256) {
     const unsigned grid = tiles(256, 256);
     fp8_tile_kernel<256, 256, F32><<<grid, 512, 0, s>>>(a);
   } else {
