@@ -24,9 +24,9 @@
 //
 // Keys that a row must not see are set to -infinity in S, so whatever K holds
 // there is replaced; their weight is then exactly 0, but 0 times an infinite or
-// NaN value would still reach the row.  So a block that masks looks at its
-// outputs once, at the end, and repeats the pass with the careful form of the
-// masked tiles only when one of them is not finite.
+// NaN value would still reach the row.  So a wave looks through the values of a
+// masked tile first and, where one is not finite, takes the product over the
+// finite ones and adds the others only to the rows that see them.
 #include <math.h>
 
 #include <algorithm>
@@ -89,6 +89,8 @@ struct AttnArgs {
   int n_seqs, q_rows, kv_rows, q_heads, kv_heads, group, max_q, max_kv, causal;
   int chunk;        // keys of a split, a multiple of the tile
   int tile_rows;    // rows of a block
+  int token;        // 1: the few-rows kernel
+  int join_rows;    // rows of a block of the join
   float scale, c;   // c = scale * log2(e)
 };
 
@@ -491,7 +493,11 @@ __global__ __launch_bounds__(64 * decode_waves<D>(), 1) void attn_token_kernel(A
   __shared__ __attribute__((aligned(1024))) uint8_t smem1[NW][2][kTile];
   __shared__ float s_m[NW][32], s_l[NW][32];
   static_assert(NW * 32 * D * 4 == sizeof(smem0), "the merge uses a stage");
-  const int kv_head = blockIdx.x % a.kv_heads, seq = blockIdx.x / a.kv_heads, split = blockIdx.y;
+  const int seq = blockIdx.x / a.kv_heads, split = blockIdx.y;
+  // Blocks are dealt to the 8 XCDs in turn; with eight key heads that would tie a
+  // head to an XCD, and the rows of one head, a power of two apart, to a part of
+  // the channels of its L2.  So the heads of each sequence and split begin elsewhere.
+  const int kv_head = (blockIdx.x + seq + split) % a.kv_heads;
   TileWork w;
   sequence(a, seq, w.q0, w.lq, w.k0, w.lk);
   w.q0 = uniform(w.q0), w.lq = uniform(w.lq), w.k0 = uniform(w.k0), w.lk = uniform(w.lk);
@@ -596,44 +602,90 @@ __global__ __launch_bounds__(64 * decode_waves<D>(), 1) void attn_token_kernel(A
 }
 
 // ---------------------------------------------------------------- the join of the splits
-// One thread per four outputs of a row: the shares of its splits, in order.
+// A thread per four outputs of a row.  It reads kJoin shares at a time, so that
+// their latencies overlap.  With few splits (a.join_rows = 256 / (D / 4) rows in
+// a block) it takes them all; with many, the block has one row, its thread
+// groups take turns over the splits and meet in LDS.  Either way in a fixed order.
+constexpr int kJoin = 8;
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-  constexpr int kPer = 256 / (D / 4);  // rows of a block
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * kPer + threadIdx.x / (D / 4);
-  const int d = 4 * (threadIdx.x % (D / 4));
-  const int64_t q_row = u / a.q_heads;
+  constexpr int kGroups = 256 / (D / 4);
+  __shared__ f32x4 s_o[kGroups][D / 4];
+  __shared__ float2 s_ml[kGroups];
+  const int grp = threadIdx.x / (D / 4), quad = threadIdx.x % (D / 4);
+  const bool shared = a.join_rows == 1;
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * a.join_rows + (shared ? 0 : grp);
+  int64_t q_row = u / a.q_heads;
   const int head = static_cast<int>(u - q_row * a.q_heads);
-  if (q_row >= a.q_rows) return;
-  // the sequence of this row: the last one that begins at or before it
-  int lo = 0, hi = a.n_seqs;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.cu_q[mid] <= q_row) lo = mid; else hi = mid;
-  }
   TileWork w;
-  sequence(a, lo, w.q0, w.lq, w.k0, w.lk);
-  const int pos = static_cast<int>(q_row) - w.q0;
+  int pos;
+  if (a.token) {  // u counts the rows below max_q of each sequence
+    const int seq = static_cast<int>(q_row / a.max_q);
+    if (seq >= a.n_seqs) return;
+    sequence(a, seq, w.q0, w.lq, w.k0, w.lk);
+    pos = static_cast<int>(q_row - static_cast<int64_t>(seq) * a.max_q);
+    q_row = w.q0 + pos;
+  } else {  // u counts q's rows: the sequence is the last one that begins at or before it
+    if (q_row >= a.q_rows) return;
+    int lo = 0, hi = a.n_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (a.cu_q[mid] <= q_row) lo = mid; else hi = mid;
+    }
+    sequence(a, lo, w.q0, w.lq, w.k0, w.lk);
+    pos = static_cast<int>(q_row) - w.q0;
+  }
   if (pos < 0 || pos >= min(w.lq, a.max_q)) return;
   // The tile kernels cut by what the tile's last row sees.
   const int last = min((pos * a.group + head % a.group) / a.tile_rows * a.tile_rows + a.tile_rows,
                        min(w.lq, a.max_q) * a.group) - 1;
   const int splits = (max(last_key(a, w, last / a.group) + 1, 0) + a.chunk - 1) / a.chunk;
   if (splits <= 1) return;  // written by its tile
-  float m = kNegInf;
-  for (int i = 0; i < splits; ++i) m = fmaxf(m, a.part_ml[part_row(a, i, q_row, head)].x);
-  const float ms = m == kNegInf ? 0.f : m;
-  float l = 0.f;
+  float m = kNegInf, l = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int i = 0; i < splits; ++i) {
-    const int64_t row = part_row(a, i, q_row, head);
-    const float2 ml = a.part_ml[row];
-    const float f = __builtin_amdgcn_exp2f((ml.x - ms) * a.c);
+  // a share (ml, p) with weight 2^((its maximum - m) c)
+  auto rescale = [&](float to) {
+    const float f = m == to ? 1.f : __builtin_amdgcn_exp2f((m - to) * a.c);
+    m = to;
+    l *= f;
+    o *= f;
+  };
+  auto add = [&](float2 ml, f32x4 p) {
+    const float f = __builtin_amdgcn_exp2f((ml.x - (m == kNegInf ? 0.f : m)) * a.c);
     l += f * ml.y;
-    o += f * *reinterpret_cast<const f32x4*>(a.part_o + row * D + d);
+    o += f * p;
+  };
+  const int step = shared ? kGroups : 1;
+  for (int i = shared ? grp : 0; i < splits; i += kJoin * step) {
+    float2 ml[kJoin];
+    f32x4 part[kJoin];
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j) {  // past the last one: that one again, not added
+      const int64_t row = part_row(a, min(i + j * step, splits - 1), q_row, head);
+      ml[j] = a.part_ml[row];
+      part[j] = *reinterpret_cast<const f32x4*>(a.part_o + row * D + 4 * quad);
+    }
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j) top = fmaxf(top, ml[j].x);
+    rescale(top);
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j)
+      if (i + j * step < splits) add(ml[j], part[j]);
   }
-  store_quad(a, q_row, head, d, o, m, l);
+  if (shared) {  // the whole block is here: it has one row
+    s_o[grp][quad] = o;
+    if (quad == 0) s_ml[grp] = make_float2(m, l);
+    __syncthreads();
+    if (grp != 0) return;
+    float top = m;
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) top = fmaxf(top, s_ml[g].x);
+    rescale(top);
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) add(s_ml[g], s_o[g][quad]);
+  }
+  store_quad(a, q_row, head, 4 * quad, o, m, l);
 }
 
 // ---------------------------------------------------------------- host
@@ -648,22 +700,37 @@ struct Plan {
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Which kernel, and how many keys a block takes.  Everything here follows
-// from the shape fields, as the workspace does.
+// from the shape fields, as the workspace does.  The keys are split where the
+// tiles alone do not fill the card.  Few rows, 8 key heads unless said (us):
+//   blocks wanted: one a CU where a block's LDS leaves no room for a second
+//     (head_dim 128: 32 x 1024 keys 24.3, with two 28.5; 256: 4 x 2048 keys 19.4,
+//     22.1), two where it does (64: 16 x 4096 keys 25.8, with one 29.1);
+//   a sequence of up to 4 units in one piece, without a join (4 x 512 keys 8.5, in
+//     halves 11.2); a longer one in pieces of at least 2 (4 x 1024 keys 12.0; one
+//     unit each 12.3, four 12.8, whole 13.0);
+//   no piece above 16 units, so that sequences of different lengths end together
+//     (64 x up to 8192 keys, head_dim 128: 236; 8 units 243, 32 units 249, whole
+//     263; head_dim 256, 32 x up to 4096: 123; 8 units 129, 32 units 141), until
+//     kRounds blocks a CU, which are even enough, and bound the workspace.
+// Many rows: pieces of at least 8 tiles of keys.
+constexpr int kRounds = 64;
+
 Plan make_plan(const moe_attn& d) {
   Plan p;
   const int64_t g = d.q_heads / d.kv_heads;
   const int64_t seqs = std::min<int64_t>(d.n_seqs, d.q_rows);
+  const int64_t keys = std::max(d.max_kv, 1);
   p.token = d.max_q * g <= kRowsD;
   p.tiles = (p.token ? d.n_seqs : seqs + d.q_rows * g / kRowsP) * d.kv_heads;
+  const int64_t tiles = std::max<int64_t>(p.tiles, 1);
   const int64_t unit = p.token ? kKeysD * (d.head_dim == 256 ? 2 : 4) : kKeysP;
-  const int64_t least = p.token ? 2 * unit : 8 * unit;   // keys that are worth a block
-  const int64_t most = p.token ? 2048 : INT32_MAX;       // and, where lengths differ, the most of one
-  const int64_t want = p.token ? 2 * kCus : 2 * kCus;    // blocks that fill the card
-  int64_t splits = std::max<int64_t>(1, ceil_div(want, std::max<int64_t>(p.tiles, 1)));
-  int64_t chunk = ceil_div(std::max(d.max_kv, 1), splits);
+  const int64_t want = p.token && d.head_dim > 64 ? kCus : 2 * kCus;
+  const int64_t least = !p.token ? 8 * unit : keys <= 4 * unit ? 4 * unit : 2 * unit;
+  const int64_t most = !p.token ? INT32_MAX : std::max(16 * unit, ceil_div(keys, std::max(kRounds * kCus / tiles, int64_t{1})));
+  int64_t chunk = ceil_div(keys, std::max<int64_t>(1, ceil_div(want, tiles)));
   chunk = std::min(std::max(chunk, least), most);
   chunk = ceil_div(chunk, unit) * unit;
-  splits = ceil_div(std::max(d.max_kv, 1), chunk);
+  const int64_t splits = ceil_div(keys, chunk);
   p.chunk = static_cast<int>(std::min<int64_t>(chunk, INT32_MAX - unit));
   p.splits = static_cast<int>(splits);
   return p;
@@ -710,8 +777,8 @@ void launch(const AttnArgs& a, const Plan& p, hipStream_t s) {
   else
     attn_rows_kernel<D><<<grid, 256, 0, s>>>(a);
   if (p.splits > 1) {
-    const int64_t rows = static_cast<int64_t>(a.q_rows) * a.q_heads;
-    attn_join_kernel<D><<<static_cast<unsigned>(ceil_div(rows * (D / 4), 256)), 256, 0, s>>>(a);
+    const int64_t rows = (p.token ? static_cast<int64_t>(a.n_seqs) * a.max_q : a.q_rows) * a.q_heads;
+    attn_join_kernel<D><<<static_cast<unsigned>(ceil_div(rows, a.join_rows)), 256, 0, s>>>(a);
   }
 }
 
@@ -781,6 +848,8 @@ int moe_attention(const moe_attn* a, void* ws, size_t ws_bytes, void* stream) {
   k.q_heads = a->q_heads, k.kv_heads = a->kv_heads, k.group = a->q_heads / a->kv_heads;
   k.max_q = a->max_q, k.max_kv = a->max_kv, k.causal = a->causal;
   k.chunk = p.chunk, k.tile_rows = p.token ? moe::kRowsD : moe::kRowsP;
+  k.token = p.token;
+  k.join_rows = p.splits > moe::kJoin ? 1 : 256 / (a->head_dim / 4);
   k.scale = a->scale;
   k.c = a->scale * 1.44269504088896340736f;  // log2(e)
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
