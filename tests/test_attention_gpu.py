@@ -540,3 +540,18 @@ def test_no_tokens():
                         torch.zeros(1, 1, dtype=torch.uint8, device="cuda")).shape == (0, 8)
     assert A.qk_norm_rope(e(0, 2, 64), e(0, 1, 64), None, None, None, None)[0].shape == (0, 2, 64)
     assert A.attention(e(0, 2, 64), e(0, 1, 64), e(0, 1, 64), z, 0).shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("lq,lk,Hq,Hkv,D", [
+    # many splits: the join shares them out over a block, and sequences that need few of them or none stand beside
+    ([1], [40000], 4, 1, 128), ([1, 1, 1], [20000, 0, 129], 8, 2, 64), ([1, 1], [300, 9000], 16, 2, 256),
+    ([6, 1], [9000, 1], 4, 1, 128), ([50, 3], [9000, 600], 2, 1, 64), ([40], [6000], 2, 1, 256)])
+def test_attention_many_splits(lq, lk, Hq, Hkv, D):
+    _say("attention many splits", lq, lk, Hq, Hkv, D)
+    g = np.random.default_rng(sum(lk) + D)
+    q0, seqs = _seqs(lq, lk, max(lk))
+    rows = len(lq) * max(lk)
+    q = R.bf16(g.normal(0, 2, (sum(lq), Hq, D)))
+    k, v = R.bf16(g.normal(0, 1, (rows, Hkv, D))), R.bf16(g.normal(0, 1, (rows, Hkv, D)))
+    out, lse = _run(_bf16(q), _bf16(k), _bf16(v), q0, seqs, True)
+    _check_attention(out, lse, q, k, v, seqs, D ** -0.5, True)
