@@ -98,8 +98,8 @@ typedef struct moe_heads {
  * q_out, k_out  out; may be q and k themselves (in place) but must not otherwise overlap them
  * Requirements: head_dim a multiple of 8 up to 512; rot_dim a multiple of 16
  * (0 = no rotation), rot_offset a multiple of 8, rot_offset + rot_dim <=
- * head_dim; 1 <= q_heads, 0 <= k_heads, q_heads + k_heads <= 1024 (MOE_ESHAPE
- * otherwise); eps >= 0 (MOE_EINVAL).
+ * head_dim; 1 <= q_heads, 0 <= k_heads, q_heads + k_heads <= 1024, T * (q_heads +
+ * k_heads) < 2^28 (MOE_ESHAPE otherwise); eps >= 0 (MOE_EINVAL).
  */
 int moe_qk_norm_rope(const moe_heads* q, int32_t q_heads, const moe_heads* k, int32_t k_heads, int32_t T,
                      int32_t head_dim, const float* q_weight, const float* k_weight, float eps,
@@ -118,8 +118,8 @@ int moe_qk_norm_rope(const moe_heads* q, int32_t q_heads, const moe_heads* k, in
  * Query head h reads key head h / (q_heads / kv_heads).  Scores, softmax and
  * sums are float32; the weights are rounded to bf16 for the matrix cores, out
  * is rounded once.  A row that sees no key (Lk = 0, or Lq > Lk and i < Lq - Lk)
- * gives zeros and lse = -infinity.  Keys and values that a row does not see never
- * reach it, infinities and NaN included.
+ * gives zeros and lse = -infinity, and so does one whose every score is -infinity.
+ * Keys and values that a row does not see never reach it, infinities and NaN included.
  *
  * A prompt: kv_start = kv_len = NULL (the keys and values of a sequence are the
  * rows cu_q names).  A chunk of a prompt, or a single token, over a cache:

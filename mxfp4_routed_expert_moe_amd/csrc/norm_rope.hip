@@ -182,8 +182,9 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormArgs a) {
 }
 
 // Lanes of work from which a group takes four heads: below, one head each
-// spreads the work over more of the card.
-constexpr int64_t kManyLanes = int64_t{1} << 18;
+// spreads the work over more of the card (40 heads of 128: 512 tokens, 2^18.3
+// lanes, 5.3 us against 6.3 with four; 1024 tokens, 2^19.3 lanes, 9.4 against 7.2).
+constexpr int64_t kManyLanes = int64_t{1} << 19;
 
 template <int L, bool INTER>
 void launch(NormArgs a, hipStream_t s) {
@@ -227,6 +228,7 @@ extern "C" int moe_qk_norm_rope(const moe_heads* q, int32_t q_heads, const moe_h
                                 void* stream) {
   if (T < 0 || q_heads < 0 || k_heads < 0 || rot_dim < 0 || rot_offset < 0 || n_positions < 0) return MOE_EINVAL;
   if (T > MOE_MAX_TOKENS || q_heads < 1 || q_heads > 1024 || k_heads > 1024 - q_heads) return MOE_ESHAPE;
+  if (static_cast<int64_t>(T) * (q_heads + k_heads) >= (1 << 28)) return MOE_ESHAPE;  // 2^32 threads
   if (head_dim < 8 || head_dim > 512 || head_dim % 8 != 0) return MOE_ESHAPE;
   if (rot_dim % 16 != 0 || rot_offset % 8 != 0 || rot_dim > head_dim || rot_offset > head_dim - rot_dim)
     return MOE_ESHAPE;

@@ -211,3 +211,8 @@ def test_reference_rope_keeps_norms_and_relative_angles():
         z, _ = R.norm_rope(x, None, [25, 29], cs, 0, inter, 0.0)
         assert np.allclose((y * y).sum(-1), 32)
         assert np.isclose(y[0, 0] @ y[1, 0], z[0, 0] @ z[1, 0])
+
+
+def test_qk_norm_rope_refuses_more_heads_than_a_grid_has():
+    assert B.MOE_MAX_TOKENS * 1024 == 1 << 28
+    assert _rope(T=B.MOE_MAX_TOKENS, Hq=1000, Hk=24) == ESHAPE
