@@ -712,7 +712,12 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //     (64 x up to 8192 keys, head_dim 128: 236; 8 units 243, 32 units 249, whole
 //     263; head_dim 256, 32 x up to 4096: 123; 8 units 129, 32 units 141), until
 //     kRounds blocks a CU, which are even enough, and bound the workspace.
-// Many rows: pieces of at least 8 tiles of keys.
+// Many rows: blocks wanted as above (head_dim 128: 288 tiles, 4 x 256 queries after
+//     4096 keys 51, with one 67; 256: 264 tiles, 512 queries after 16384 keys 174,
+//     with two 191); pieces of at least tiles / 16 key tiles, 4 to 16, as a join
+//     costs more the more rows there are (32 row tiles, 2 x 64 queries, 2048 keys, 4:
+//     13.2, 8: 15.8, 16: 21.4; 144, a prompt of 1024, 4: 17.8, 8: 16.9, 16: 17.9;
+//     264, a prompt of 1024, 8: 35.4, 16: 28.2).
 constexpr int kRounds = 64;
 
 Plan make_plan(const moe_attn& d) {
@@ -724,9 +729,10 @@ Plan make_plan(const moe_attn& d) {
   p.tiles = (p.token ? d.n_seqs : seqs + d.q_rows * g / kRowsP) * d.kv_heads;
   const int64_t tiles = std::max<int64_t>(p.tiles, 1);
   const int64_t unit = p.token ? kKeysD * (d.head_dim == 256 ? 2 : 4) : kKeysP;
-  const int64_t want = p.token && d.head_dim > 64 ? kCus : 2 * kCus;
-  const int64_t least = !p.token ? 8 * unit : keys <= 4 * unit ? 4 * unit : 2 * unit;
-  const int64_t most = !p.token ? INT32_MAX : std::max(16 * unit, ceil_div(keys, std::max(kRounds * kCus / tiles, int64_t{1})));
+  const int64_t want = d.head_dim > (p.token ? 64 : 128) ? kCus : 2 * kCus;
+  const int64_t least = !p.token ? std::min(std::max(tiles / 16, int64_t{4}), int64_t{16}) * unit : keys <= 4 * unit ? 4 * unit : 2 * unit;
+  const int64_t most = !p.token ? INT32_MAX
+                                : std::max(16 * unit, ceil_div(keys, std::max(kRounds * kCus / tiles, int64_t{1})));
   int64_t chunk = ceil_div(keys, std::max<int64_t>(1, ceil_div(want, tiles)));
   chunk = std::min(std::max(chunk, least), most);
   chunk = ceil_div(chunk, unit) * unit;
