@@ -604,9 +604,12 @@ __global__ __launch_bounds__(64 * decode_waves<D>(), 1) void attn_token_kernel(A
 // ---------------------------------------------------------------- the join of the splits
 // A thread per four outputs of a row.  It reads kJoin shares at a time, so that
 // their latencies overlap.  With few splits (a.join_rows = 256 / (D / 4) rows in
-// a block) it takes them all; with many, the block has one row, its thread
-// groups take turns over the splits and meet in LDS.  Either way in a fixed order.
-constexpr int kJoin = 8;
+// a block) it takes them all; with more than kJoinShared the block has one row,
+// and its thread groups take turns over the splits and meet in LDS.  Either way in
+// a fixed order.  (Whole call, shared out or not: 128 queries over 8192 keys, 13
+// splits, 39.8 against 35.7 us; one query over 65536 keys, 32 splits, 60.3 against
+// 63.1; one over 16384 keys of 256, 128 splits, 17.0 against 27.5.)
+constexpr int kJoin = 8, kJoinShared = 2 * kJoin;
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   constexpr int kGroups = 256 / (D / 4);
@@ -660,18 +663,21 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     float2 ml[kJoin];
     f32x4 part[kJoin];
 #pragma unroll
-    for (int j = 0; j < kJoin; ++j) {  // past the last one: that one again, not added
-      const int64_t row = part_row(a, min(i + j * step, splits - 1), q_row, head);
-      ml[j] = a.part_ml[row];
-      part[j] = *reinterpret_cast<const f32x4*>(a.part_o + row * D + 4 * quad);
+    for (int j = 0; j < kJoin; ++j) {
+      ml[j] = make_float2(kNegInf, 0.f);
+      part[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (i + j * step < splits) {
+        const int64_t row = part_row(a, i + j * step, q_row, head);
+        ml[j] = a.part_ml[row];
+        part[j] = *reinterpret_cast<const f32x4*>(a.part_o + row * D + 4 * quad);
+      }
     }
     float top = m;
 #pragma unroll
     for (int j = 0; j < kJoin; ++j) top = fmaxf(top, ml[j].x);
     rescale(top);
 #pragma unroll
-    for (int j = 0; j < kJoin; ++j)
-      if (i + j * step < splits) add(ml[j], part[j]);
+    for (int j = 0; j < kJoin; ++j) add(ml[j], part[j]);
   }
   if (shared) {  // the whole block is here: it has one row
     s_o[grp][quad] = o;
@@ -855,7 +861,7 @@ int moe_attention(const moe_attn* a, void* ws, size_t ws_bytes, void* stream) {
   k.max_q = a->max_q, k.max_kv = a->max_kv, k.causal = a->causal;
   k.chunk = p.chunk, k.tile_rows = p.token ? moe::kRowsD : moe::kRowsP;
   k.token = p.token;
-  k.join_rows = p.splits > moe::kJoin ? 1 : 256 / (a->head_dim / 4);
+  k.join_rows = p.splits > moe::kJoinShared ? 1 : 256 / (a->head_dim / 4);
   k.scale = a->scale;
   k.c = a->scale * 1.44269504088896340736f;  // log2(e)
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
