@@ -139,6 +139,8 @@ struct LinearArgs {
   const uint32_t* scales;  // [kb, T]
   int T, N, K, kb;         // kb: blocks of K
   int n_tiles, t_tiles;
+  int splits, chunk;       // of K: a split takes chunk blocks
+  f32x4* part;             // [splits, tiles, BN BT / 4]: the splits' sums
   bool wide;               // rows of y take 8-byte stores
 };
 
@@ -146,14 +148,16 @@ struct LinearArgs {
 // A block holds 16 NI rows of W and 16 MT tokens; its NW waves take the blocks of
 // K in turn, straight from memory, and meet in LDS.  W is read once per token
 // block: the kernel streams it.  QUANT: the block quantises x itself, into LDS,
-// while its first loads of W are on their way.
+// while its first loads of W are on their way.  Bound by latency (1 x 6144 x 4096: 7.9
+// us, 3.2 TB/s, of which 3.8 us are left with W in the cache) and, with more tokens, by x,
+// which every block reads whole from its L2 (16 x 6144 x 4096: 13.1 us).
 constexpr int kNW = 8;
 constexpr int kFusedBytes = 16 << 10;  // codes of x that the block quantises itself
 
 template <int MT, int NI, bool F32, bool QUANT>
 __global__ __launch_bounds__(64 * kNW) void fp8_few_kernel(LinearArgs a) {
   static_assert(MT * NI <= kNW, "a wave per tile at the end");
-  constexpr int kU = MT * NI <= 4 ? 4 : 2;  // blocks of K in flight per wave
+  constexpr int kU = MT <= 2 ? 4 : 2;  // blocks of K in flight per wave
   __shared__ f32x4 part[kNW][MT * NI][64];
   __shared__ __attribute__((aligned(16))) uint8_t q_codes[QUANT ? kFusedBytes : 16];
   __shared__ uint32_t q_scales[QUANT ? kFusedBytes / 128 : 1];
@@ -180,7 +184,8 @@ __global__ __launch_bounds__(64 * kNW) void fp8_few_kernel(LinearArgs a) {
   auto load_w = [&](int b0) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int b = min(b0 + u * kNW, a.kb - 1), k = 128 * b + 32 * g;
+      const int b = b0 + u * kNW, k = 128 * b + 32 * g;
+      if (b >= a.kb) break;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         wv[u][i][0] = ld16(wp[i] + min(k, last));
@@ -213,7 +218,8 @@ __global__ __launch_bounds__(64 * kNW) void fp8_few_kernel(LinearArgs a) {
     uint32_t sx[kU][MT];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int b = min(b0 + u * kNW, a.kb - 1);
+      const int b = b0 + u * kNW;
+      if (b >= a.kb) break;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const int t = min(t0 + 16 * m + r, a.T - 1);
@@ -281,6 +287,17 @@ __global__ __launch_bounds__(64 * kNW) void fp8_few_kernel(LinearArgs a) {
 // the compiler then knows that a DMA in flight does not write what is read.
 __device__ __forceinline__ int slot(int r, int c) { return c ^ ((r >> 1) & 7); }
 
+// Consecutive tiles cover kBand token tiles before the next rows of W, so that
+// the blocks an XCD runs at once share both operands in its L2.
+template <int BN, int BT>
+__device__ __forceinline__ void tile_place(const LinearArgs& a, int tile, int& n0, int& t0) {
+  constexpr int kBand = 4;
+  const int band = tile / (kBand * a.n_tiles), in_band = tile - band * kBand * a.n_tiles;
+  const int wide = min(kBand, a.t_tiles - kBand * band);
+  t0 = __builtin_amdgcn_readfirstlane((kBand * band + in_band % wide) * BT);
+  n0 = __builtin_amdgcn_readfirstlane((in_band / wide) * BN);
+}
+
 template <int BN, int BT, bool F32>
 __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(LinearArgs a) {
   constexpr int kN = BN / 32, kT = BT / 64;        // 16 x 16 tiles of a wave
@@ -301,16 +318,14 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(LinearArgs a) {
   const int r = lane & 15, g = lane >> 4;
 
   // Blocks are dealt to the 8 XCDs in turn: each XCD gets a run of consecutive
-  // units, and a run covers kBand token tiles before it goes to the next rows
-  // of W, so that the blocks an XCD runs at once share both operands in its L2.
-  constexpr int kBand = 4;
-  const int total = a.n_tiles * a.t_tiles, per = (total + 7) >> 3;
+  // units, the tiles of one split of K after those of another.
+  const int tiles = a.n_tiles * a.t_tiles, total = tiles * a.splits, per = (total + 7) >> 3;
   const int unit = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
   if ((blockIdx.x >> 3) >= per || unit >= total) return;
-  const int band = unit / (kBand * a.n_tiles), in_band = unit - band * kBand * a.n_tiles;
-  const int wide = min(kBand, a.t_tiles - kBand * band);
-  const int t0 = __builtin_amdgcn_readfirstlane((kBand * band + in_band % wide) * BT);
-  const int n0 = __builtin_amdgcn_readfirstlane((in_band / wide) * BN);
+  const int split = unit / tiles;
+  const int begin = split * a.chunk, end = min(a.kb, begin + a.chunk);  // of the blocks of K
+  int n0, t0;
+  tile_place<BN, BT>(a, unit - split * tiles, n0, t0);
 
   // W's scales of the two groups' rows
   for (int i = threadIdx.x; i < 2 * a.kb; i += 512) {
@@ -331,7 +346,7 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(LinearArgs a) {
     int row = row0;
     asm volatile("" : "+v"(row));  // derived offsets are not kept in registers from step to step
     const __amdgpu_buffer_rsrc_t src =
-        raw_buffer(a.w + static_cast<int64_t>(n0 + h * (BN / 2)) * a.K, b < a.kb ? w_bytes[h] : 0);
+        raw_buffer(a.w + static_cast<int64_t>(n0 + h * (BN / 2)) * a.K, b < end ? w_bytes[h] : 0);
     const int k = row * a.K + min(128 * b + 16 * slot(row, lane & 7), a.K - 16);
 #pragma unroll
     for (int i = 0; i < kWOps; ++i) dma16(src, k + 64 * i * a.K, 0, to + 1024 * (8 * i + wave));
@@ -341,7 +356,7 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(LinearArgs a) {
     int row = row0;
     asm volatile("" : "+v"(row));
     const int64_t first = static_cast<int64_t>(b) * a.T + t0;
-    const int rows = b < a.kb ? x_rows : 0;
+    const int rows = b < end ? x_rows : 0;
     const __amdgpu_buffer_rsrc_t src = raw_buffer(a.codes + 128 * first, 128 * rows);
 #pragma unroll
     for (int i = 0; i < kXOps; ++i)
@@ -424,13 +439,13 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(LinearArgs a) {
     stage_barrier();
   };
 
-  issue_w(0, wa0, 0);
-  issue_x(x0, 0);
-  issue_w(1, wb0, 0);
-  issue_w(0, wa1, 1);
+  issue_w(0, wa0, begin);
+  issue_x(x0, begin);
+  issue_w(1, wb0, begin);
+  issue_w(0, wa1, begin + 1);
   wait_vmcnt<0>();
   stage_barrier();
-  int b = 0;
+  int b = begin;
   if (group == 0) {
     auto step = [&](const Tokens& x, uint8_t* wa, Tokens& xn, uint8_t* wbn) __attribute__((always_inline)) {
       issue_x(xn, b + 1);
@@ -442,32 +457,40 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(LinearArgs a) {
       end_odd();
       ++b;
     };
-    while (b + 1 < a.kb) {
+    while (b + 1 < end) {
       step(x0, wa0, x1, wb1);
       step(x1, wa1, x0, wb0);
     }
-    if (b < a.kb) step(x0, wa0, x1, wb1);
+    if (b < end) step(x0, wa0, x1, wb1);
   } else {
     auto step = [&](const Tokens& x, const uint8_t* wb, uint8_t* wa, Tokens& xn,
                     uint8_t* wbn) __attribute__((always_inline)) {
       issue_x(xn, b + 1);
       issue_w(1, wbn, b + 1);
-      if (b > 0) multiply();
+      if (b > begin) multiply();
       end_even();
       issue_w(0, wa, b + 2);
       read(x, wb, b);
       end_odd();
       ++b;
     };
-    while (b + 1 < a.kb) {
+    while (b + 1 < end) {
       step(x0, wb0, wa0, x1, wb1);
       step(x1, wb1, wa1, x0, wb0);
     }
-    if (b < a.kb) step(x0, wb0, wa0, x1, wb1);
+    if (b < end) step(x0, wb0, wa0, x1, wb1);
     multiply();
   }
   wait_vmcnt<0>();  // no DMA is left for the LDS of the next block
 
+  if (BT == 64 && a.splits > 1) {
+    f32x4* p = a.part + static_cast<int64_t>(unit) * (BN * BT / 4) + wave * (64 * kN * kT) + lane;
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+#pragma unroll
+      for (int j = 0; j < kT; ++j) p[64 * (i * kT + j)] = acc[i][j];
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < kT; ++j) {
     const int t = t0 + (BT / 4) * wt + 16 * j + r;
@@ -480,6 +503,27 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(LinearArgs a) {
   }
 }
 
+// The sum of the splits, in order.  A block takes the tiles of one wave of one tile
+// of the kernel above, and finds their places as that does.
+template <int BN, int BT>
+__global__ __launch_bounds__(256) void fp8_join_kernel(LinearArgs a) {
+  constexpr int kN = BN / 32, kT = BT / 64;
+  static_assert(kN * kT % 4 == 0, "four waves share the tiles");
+  const int tiles = a.n_tiles * a.t_tiles, tile = blockIdx.x >> 3, wave = blockIdx.x & 7;
+  int n0, t0;
+  tile_place<BN, BT>(a, tile, n0, t0);
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int u = threadIdx.x >> 6; u < kN * kT; u += 4) {
+    const f32x4* p = a.part + static_cast<int64_t>(tile) * (BN * BT / 4) + wave * (64 * kN * kT) + 64 * u + lane;
+    f32x4 v = p[0];
+    for (int i = 1; i < a.splits; ++i) v += p[static_cast<int64_t>(i) * tiles * (BN * BT / 4)];
+    const int t = t0 + (BT / 4) * (wave & 3) + 16 * (u % kT) + r;
+    const int n = n0 + (wave >> 2) * (BN / 2) + 16 * (u / kT) + 4 * g;
+    if (t < a.T) store4(a.y, a.y_stride, t, n, a.N, a.wide, v);
+  }
+}
+
 // ---------------------------------------------------------------- host
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t align256(size_t v) { return (v + 255) & ~size_t{255}; }
@@ -489,18 +533,39 @@ bool shape_ok(int32_t T, int32_t N, int32_t K) {
   return T >= 0 && T <= MOE_MAX_TOKENS && N > 0 && N <= MOE_MAX_DIM && K > 0 && K <= MOE_MAX_DIM && K % 16 == 0;
 }
 
-// Which kernel, by how many blocks there are to fill the card (microseconds at K =
-// 4096, E8M0 scales, quantisation included):
-//   few-token kernel against 128 x 128 tiles, by the number of those tiles: 32
-//   tiles (T = 512, N = 1024) 17.5 against 24.6, 64 tiles (T = 256, N = 4096) 30.0
-//   against 29.0, 96 tiles (T = 256, N = 6144) 44.4 against 31.8;
-//   128 x 128 against 256 x 256 tiles, by the number of the latter: 96 tiles (T =
-//   1024, N = 6144) 45.6 against 59.4, 128 tiles (T = 2048, N = 4096) 50.9 against
-//   61.6, 192 tiles (T = 2048, N = 6144) 75.3 against 66.2;
-//   one or two row tiles of W per block of the few-token kernel, by the blocks with
-//   two: 128 blocks (T = 64, N = 4096) 15.6 against 16.8, 252 blocks (T = 509,
-//   N = 1000, K = 2064) 14.5 against 10.2.
-constexpr int64_t kTiles128 = 64, kTiles256 = 192, kFillCard = 192;
+// Which kernel (microseconds of a call with E8M0 scales, quantisation and join
+// included, T x N x K).
+//   Up to 16 tokens: the few-token kernel (16 x 6144 x 4096 13.1, 128 x 64 tiles 16.6;
+//   16 x 4096 x 16384 24.1, 25.5).  Beyond, where its blocks are on the card at once and K
+//   is short enough for a block of it: 17 to 32 tokens up to 48 blocks of K (32 x 4096 x 4096
+//   10.7, tiles 14.0; 32 x 1024 x 8192 15.5, 13.5; 512 blocks, 32 x 8192 x 8192, 31.6, 25.3),
+//   more tokens up to 24 (512 x 1024 x 2064 10.3, tiles 13.3; 128 x 4096 x 4096 16.9, 15.7;
+//   512 blocks, 512 x 2048 x 2048, 17.7, 15.3).
+//   128 x 64 tiles, K split over the card, below kTiles128 tiles of 128 x 128 (96 of
+//   them, 768 x 2048 x 2048, 14.4, with 128 x 128 18.9; 160, 640 x 4096 x 4096, 32.4,
+//   31.6; 256, 1024 x 4096 x 4096, 35.9, 33.1).
+//   256 x 256 tiles from kTiles256 of them (128 tiles, 2048 x 4096 x 4096, 61.6, with
+//   128 x 128 51.0; 160, 1280 x 8192 x 4096, 61.8, 65.9).
+constexpr int64_t kCus = 256, kTiles128 = 160, kTiles256 = 160;
+
+bool few_tokens(int64_t T, int64_t N, int64_t kb) {
+  if (T <= 16) return true;
+  if (T <= 32) return ceil_div(N, 16) <= kCus && kb <= 48;
+  return ceil_div(N, 32) * ceil_div(T, 64) <= kCus && kb <= 24;
+}
+
+// Splits of K for 128 x 64 tiles: one block per CU, of at least 4 blocks of K (64 x
+// 2048 x 2048 10.4; of at least 8 11.6; 64 x 8192 x 4096 18.4, two blocks per CU 20.7).
+int splits_of(int64_t tiles, int64_t kb) {
+  return static_cast<int>(std::max<int64_t>(1, std::min(kCus / tiles, kb / 4)));
+}
+
+// Room for the splits' sums of any call with up to T tokens, N rows and kb blocks of K.
+size_t part_bytes(int64_t T, int64_t N, int64_t kb) {
+  if (T <= 16) return 0;
+  const int64_t tiles = ceil_div(N, 128) * ceil_div(T, 64);
+  return static_cast<size_t>(std::min(kCus, tiles * std::max<int64_t>(kb / 4, 1))) * (128 * 64 * 4);
+}
 
 template <bool F32>
 void launch(LinearArgs& a, hipStream_t s) {
@@ -510,29 +575,33 @@ void launch(LinearArgs& a, hipStream_t s) {
   }
   fp8_quant_kernel<F32><<<static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.T) * a.kb, 16)), 256, 0, s>>>(
       a.x, a.x_stride, a.T, a.K, a.kb, const_cast<uint8_t*>(a.codes), const_cast<uint32_t*>(a.scales));
-  if (a.T <= 64 || ceil_div(a.N, 128) * ceil_div(a.T, 128) < kTiles128) {
-    const unsigned t64 = static_cast<unsigned>(ceil_div(a.T, 64));
+  if (few_tokens(a.T, a.N, a.kb)) {
     if (a.T <= 16)
       fp8_few_kernel<1, 1, F32, false><<<dim3(ceil_div(a.N, 16), 1), 64 * kNW, 0, s>>>(a);
     else if (a.T <= 32)
       fp8_few_kernel<2, 1, F32, false><<<dim3(ceil_div(a.N, 16), 1), 64 * kNW, 0, s>>>(a);
-    else if (ceil_div(a.N, 32) * t64 < kFillCard)
-      fp8_few_kernel<4, 1, F32, false><<<dim3(ceil_div(a.N, 16), t64), 64 * kNW, 0, s>>>(a);
     else
-      fp8_few_kernel<4, 2, F32, false><<<dim3(ceil_div(a.N, 32), t64), 64 * kNW, 0, s>>>(a);
+      fp8_few_kernel<4, 2, F32, false><<<dim3(ceil_div(a.N, 32), ceil_div(a.T, 64)), 64 * kNW, 0, s>>>(a);
     return;
   }
-  auto tiles = [&](int bn, int bt) {
+  auto tiles = [&](int bn, int bt, int splits) {
     a.n_tiles = static_cast<int>(ceil_div(a.N, bn));
     a.t_tiles = static_cast<int>(ceil_div(a.T, bt));
-    return static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.n_tiles) * a.t_tiles, 8) * 8);
+    a.chunk = static_cast<int>(ceil_div(a.kb, splits));
+    a.splits = static_cast<int>(ceil_div(a.kb, a.chunk));
+    return static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.n_tiles) * a.t_tiles * a.splits, 8) * 8);
   };
   if (ceil_div(a.N, 256) * ceil_div(a.T, 256) >= kTiles256) {
-    const unsigned grid = tiles(256, 256);
+    const unsigned grid = tiles(256, 256, 1);
     fp8_tile_kernel<256, 256, F32><<<grid, 512, 0, s>>>(a);
-  } else {
-    const unsigned grid = tiles(128, 128);
+  } else if (ceil_div(a.N, 128) * ceil_div(a.T, 128) >= kTiles128) {
+    const unsigned grid = tiles(128, 128, 1);
     fp8_tile_kernel<128, 128, F32><<<grid, 512, 0, s>>>(a);
+  } else {
+    const unsigned grid = tiles(128, 64, splits_of(ceil_div(a.N, 128) * ceil_div(a.T, 64), a.kb));
+    fp8_tile_kernel<128, 64, F32><<<grid, 512, 0, s>>>(a);
+    if (a.splits > 1)
+      fp8_join_kernel<128, 64><<<static_cast<unsigned>(a.n_tiles * a.t_tiles) * 8, 256, 0, s>>>(a);
   }
 }
 
@@ -544,7 +613,8 @@ extern "C" {
 size_t moe_fp8_linear_workspace_size(int32_t T, int32_t N, int32_t K) {
   if (!moe::shape_ok(T, N, K) || T <= 0) return 0;
   const size_t kb = moe::ceil_div(K, 128);
-  return moe::align256(static_cast<size_t>(T) * kb * 128) + moe::align256(static_cast<size_t>(T) * kb * 4);
+  return moe::align256(static_cast<size_t>(T) * kb * 128) + moe::align256(static_cast<size_t>(T) * kb * 4) +
+         moe::part_bytes(T, N, kb);
 }
 
 int moe_fp8_linear(const uint16_t* x, int64_t x_stride, int32_t T, int32_t K, const uint8_t* w, const void* w_scale,
@@ -566,7 +636,10 @@ int moe_fp8_linear(const uint16_t* x, int64_t x_stride, int32_t T, int32_t K, co
   a.T = T, a.N = N, a.K = K, a.kb = static_cast<int>(moe::ceil_div(K, 128));
   a.codes = static_cast<const uint8_t*>(ws);
   a.scales = reinterpret_cast<const uint32_t*>(a.codes + moe::align256(static_cast<size_t>(T) * a.kb * 128));
+  a.part = reinterpret_cast<moe::f32x4*>(static_cast<char*>(ws) + moe::align256(static_cast<size_t>(T) * a.kb * 128) +
+                                    moe::align256(static_cast<size_t>(T) * a.kb * 4));
   a.n_tiles = a.t_tiles = 0;
+  a.splits = 1, a.chunk = a.kb;
   a.wide = y_stride % 4 == 0 && moe::aligned(y, 8);
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (scale_type == MOE_SCALE_F32)

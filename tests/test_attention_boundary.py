@@ -216,3 +216,14 @@ def test_reference_rope_keeps_norms_and_relative_angles():
 def test_qk_norm_rope_refuses_more_heads_than_a_grid_has():
     assert B.MOE_MAX_TOKENS * 1024 == 1 << 28
     assert _rope(T=B.MOE_MAX_TOKENS, Hq=1000, Hk=24) == ESHAPE
+
+
+def test_fp8_linear_workspace_grows_with_every_size():
+    """A workspace for up to T tokens serves fewer of them, as for N and K."""
+    sizes = (1, 16, 17, 64, 65, 130, 500, 700, 5000, 20000)
+    f = A.fp8_linear_workspace_size
+    for n, k in ((16, 16), (1000, 2064), (4096, 4096), (16384, 16384)):
+        got = [f(t, n, k) for t in sizes]
+        assert got == sorted(got)
+        for t in sizes:
+            assert f(t, n, k) <= f(t, n + 1000 if n < 15000 else n, k) and f(t, n, k) <= f(t, n, min(k + 1600, 16384))

@@ -555,3 +555,21 @@ def test_attention_many_splits(lq, lk, Hq, Hkv, D):
     k, v = R.bf16(g.normal(0, 1, (rows, Hkv, D))), R.bf16(g.normal(0, 1, (rows, Hkv, D)))
     out, lse = _run(_bf16(q), _bf16(k), _bf16(v), q0, seqs, True)
     _check_attention(out, lse, q, k, v, seqs, D ** -0.5, True)
+
+
+@pytest.mark.parametrize("kind", ["e8m0", "float32"])
+@pytest.mark.parametrize("T,N,K", [
+    # K split over the card (several blocks of a split, a last one of fewer, one of a partial block), and every tile size
+    (20, 4200, 400), (33, 300, 8208), (64, 130, 16384), (65, 1000, 4112), (130, 257, 2560), (300, 1025, 1552),
+    (1100, 2300, 272), (2500, 4100, 272)])
+def test_fp8_linear_tiles_and_splits(T, N, K, kind):
+    _say("fp8_linear tiles", T, N, K, kind)
+    g = np.random.default_rng(T * 7919 + N * 31 + K)
+    x = R.bf16(g.normal(0, 1, (T, K)) * np.exp(g.normal(0, 1, K)))
+    codes, s, sv = _weights(g, N, K, kind)
+    y = A.fp8_linear(_bf16(x), _gpu(codes), _gpu(s))
+    again = A.fp8_linear(_bf16(x), _gpu(codes), _gpu(s))
+    assert torch.equal(y, again)
+    rows = np.unique(np.r_[0, T - 1, g.integers(0, T, 40)])
+    ref, mag, top = R.fp8_linear(x[rows], codes, sv, kind)
+    _check_linear(y[torch.from_numpy(rows).cuda()], ref, mag, top, K)
