@@ -100,8 +100,8 @@ class AttentionBlock:
     def workspace(self, plan: Plan):
         """The attention workspace of a plan, for callers that keep it."""
         n = plan.rows.numel()
-        return A.attention_workspace(self.qkv[:n, :self.Hq], self.cache[:, :self.Hkv], plan.cu_q.numel() - 1, plan.max_q,
-                                     plan.max_kv)
+        return A.attention_workspace(self.qkv[:n, :self.Hq], self.cache[:, :self.Hkv], plan.cu_q.numel() - 1,
+                                     plan.max_q, plan.max_kv)
 
     def forward(self, x, plan: Plan, ws=None):
         """x bf16 [tokens of the plan, hidden] -> y of the same shape, a view of
@@ -115,7 +115,8 @@ class AttentionBlock:
         A.qk_norm_rope(q, k, self.q_weight, self.k_weight, plan.positions, self.cos_sin, q_out=q, k_out=k, **self.rope)
         self.cache.index_copy_(0, plan.rows, qkv[:, Hq:])
         A.attention(q, self.cache[:, :Hkv], self.cache[:, Hkv:], plan.cu_q, plan.max_q,
-                    kv_start=self.kv_start[:plan.cu_q.numel() - 1], kv_len=plan.kv_len, max_kv=plan.max_kv, out=o, ws=ws)
+                    kv_start=self.kv_start[:plan.cu_q.numel() - 1], kv_len=plan.kv_len, max_kv=plan.max_kv, out=o,
+                    ws=ws)
         return A.fp8_linear(o.view(T, -1), self.w_out, self.out_scale, y=y, ws=self.ws)
 
 

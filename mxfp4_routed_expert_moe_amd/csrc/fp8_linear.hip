@@ -13,9 +13,9 @@
 //
 // Past the end of K the quantised x is zero (its rows are padded to whole
 // blocks), and W repeats its row's last 16 bytes: zero times a weight the row holds
-// anyway.  Past the end of N and T the last row is repeated and not stored.
+// anyway.  Past the end of N and T the last row is repeated, or zeros are read, and
+// nothing is stored.
 #include <algorithm>
-#include <type_traits>
 
 #include "../../include/moe_attention.h"
 #include "lds_dma.h"
@@ -66,7 +66,8 @@ __device__ __forceinline__ float max_abs(u32x4 w, float m) {
 // codes [kb, T, 128] (the last block padded with zeros), scales [kb, T].  Block by
 // block, so that the rows a tile kernel reads at once are contiguous: rows K
 // bytes apart would fall on few of the L2's channels.  16 lanes per block, 8
-// values each.
+// values each.  Bound by HBM: 16384 x 4096 are 203 MB in 38 us = 5.3 TB/s (two, four or
+// eight blocks per lane group the same).
 template <bool F32>
 __global__ __launch_bounds__(256) void fp8_quant_kernel(const uint16_t* __restrict__ x, int64_t x_stride, int T, int K,
                                                         int kb, uint8_t* __restrict__ codes,
@@ -291,6 +292,12 @@ __global__ __launch_bounds__(64 * kNW) void fp8_few_kernel(LinearArgs a) {
 // phase 2 b + 1.  The loads return in order, so a wait names how many of the
 // latest may still be out.
 //
+// With 256 x 256 tiles the steps are bound by the copies into LDS, 64 KB of them from L2
+// per CU and step: 16384 x 6144 x 4096 takes 350 us beside 38 of quantisation = 2.3
+// PFLOP/s (a library product of quantised operands with one scale each: 344 us),
+// 4096^3 with float32 scales 67 us beside 14 = 2.05 PFLOP/s (library: 54).  128 x 64 tiles with K
+// split are bound by the latency of a step, about 0.6 us.
+//
 // Layout: rows of 128 bytes, 16-byte chunk c of row r in slot c ^ ((r / 2) mod 8),
 // which spreads the 16 rows of a fragment read over all banks.  An operand's lane
 // (r, g) holds chunks g and 4 + g of row r.  Every part is a variable of its own:
@@ -311,7 +318,7 @@ __device__ __forceinline__ void tile_place(const LinearArgs& a, int tile, int& n
 template <int BN, int BT, bool F32>
 __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(LinearArgs a) {
   constexpr int kN = BN / 32, kT = BT / 64;        // 16 x 16 tiles of a wave
-  constexpr int kWOps = BN / 128, kXOps = BT / 64;  // DMA instructions of a wave, 8 rows each: a group's rows; the tokens
+  constexpr int kWOps = BN / 128, kXOps = BT / 64;  // DMA instructions of a wave: a group's rows; the tokens
   struct Tokens {
     uint8_t x[BT * 128];
     uint32_t s[BT];
