@@ -292,11 +292,12 @@ __global__ __launch_bounds__(64 * kNW) void fp8_few_kernel(LinearArgs a) {
 // phase 2 b + 1.  The loads return in order, so a wait names how many of the
 // latest may still be out.
 //
-// With 256 x 256 tiles the steps are bound by the copies into LDS, 64 KB of them from L2
-// per CU and step: 16384 x 6144 x 4096 takes 350 us beside 38 of quantisation = 2.3
-// PFLOP/s (a library product of quantised operands with one scale each: 344 us),
-// 4096^3 with float32 scales 67 us beside 14 = 2.05 PFLOP/s (library: 54).  128 x 64 tiles with K
-// split are bound by the latency of a step, about 0.6 us.
+// With 256 x 256 tiles the steps are bound by the copies into LDS, 64 KB of them from
+// L2 per CU and step: 16384 x 6144 x 4096 takes 391 to 412 us with its 40 of
+// quantisation, 2.2 to 2.35 PFLOP/s for the product (a library product of quantised
+// operands with one scale each: 344 us), 4096^3 with float32 scales 79 to 84 with its 14, 2.0 to
+// 2.1 PFLOP/s (library: 54).  128 x 64 tiles with K split are bound by the latency of
+// a step, about 0.6 us.
 //
 // Layout: rows of 128 bytes, 16-byte chunk c of row r in slot c ^ ((r / 2) mod 8),
 // which spreads the 16 rows of a fragment read over all banks.  An operand's lane
