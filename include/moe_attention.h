@@ -146,7 +146,7 @@ typedef struct moe_attn {
   int32_t max_q;          /* 0 .. q_rows */
   int32_t max_kv;         /* 0 .. kv_rows */
   int32_t causal;         /* 0 or 1 */
-  float scale;            /* > 0, finite */
+  float scale;            /* > 0, at most 2^127 */
   int32_t reserved;       /* 0 */
   moe_heads q, k, v, out; /* out: must not overlap the others; row_stride of k and v at most 2^23 */
   const int32_t* cu_q;

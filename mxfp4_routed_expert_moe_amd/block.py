@@ -26,18 +26,32 @@ class Plan:
     """The tokens of one call, sequence after sequence, and where they go.
 
     cu_q, kv_len, positions and rows are int32 (rows: int64) device tensors;
-    max_q and max_kv bound the sequences' new tokens and cached lengths."""
+    max_q and max_kv bound the sequences' new tokens and cached lengths.  The
+    block that made the plan knows how many tokens each sequence holds; advance
+    and replayed keep that in step."""
 
-    def __init__(self, cu_q, kv_len, positions, rows, max_q, max_kv):
+    def __init__(self, block, new, cu_q, kv_len, positions, rows, max_q, max_kv):
+        self.block, self.new = block, list(new)
         self.cu_q, self.kv_len, self.positions, self.rows = cu_q, kv_len, positions, rows
         self.max_q, self.max_kv = max_q, max_kv
+        self.longest = max(block.lens[:len(self.new)], default=0)
 
     def advance(self):
-        """The same call one token later (single-token plans): three additions on
-        the current stream.  The caller keeps the lengths within max_kv."""
+        """The same call one token later (plans of at most one token per
+        sequence): three additions on the current stream.  The last step is the
+        one whose longest sequence holds max_kv tokens."""
+        self.replayed(1)
         self.positions.add_(1)
         self.kv_len.add_(1)
         self.rows.add_(1)
+
+    def replayed(self, steps: int):
+        """Note `steps` replays of a HIP graph that holds advance()."""
+        if any(n > 1 for n in self.new):
+            raise ValueError("a plan of more than one token per sequence cannot be advanced")
+        for b, n in enumerate(self.new):
+            self.block.lens[b] += n * steps
+        self.longest += steps
 
 
 class AttentionBlock:
@@ -65,7 +79,7 @@ class AttentionBlock:
         self.rope = dict(rot_offset=rot_offset, interleaved=interleaved, eps=eps)
         self.max_seqs, self.max_len, self.max_tokens = max_seqs, max_len, max_tokens
         dev, bf16 = w_qkv.device, torch.bfloat16
-        self.lens = [0] * max_seqs  # tokens that each sequence's plans have brought
+        self.lens = [0] * max_seqs  # tokens that each sequence holds once its plans have run
         self.cache = torch.empty((max_seqs * max_len, 2 * kv_heads, head_dim), dtype=bf16, device=dev)
         self.kv_start = torch.arange(0, max_seqs * max_len, max_len, dtype=torch.int32, device=dev)
         self.qkv = torch.empty((max_tokens, q_heads + 2 * kv_heads, head_dim), dtype=bf16, device=dev)
@@ -76,9 +90,9 @@ class AttentionBlock:
 
     def plan(self, new, max_kv=None) -> Plan:
         """A call that brings new[b] tokens to sequence b, after those that earlier
-        plans brought (host list; fewer entries than max_seqs: the first ones).
-        max_kv: the bound on the cached lengths, this call's by default; a plan
-        that is to be advanced passes the one of its last step."""
+        plans and their advances brought (host list; fewer entries than max_seqs: the
+        first ones).  max_kv: the bound on the cached lengths, this call's by
+        default; a plan that is to be advanced passes the one of its last step."""
         if len(new) > self.max_seqs or any(n < 0 for n in new):
             raise ValueError(f"new must hold up to {self.max_seqs} counts")
         if sum(new) > self.max_tokens:
@@ -86,6 +100,11 @@ class AttentionBlock:
         ends = [have + n for have, n in zip(self.lens, new)]
         if any(e > self.max_len for e in ends):
             raise ValueError(f"a sequence would hold {max(ends)} tokens, the cache has room for {self.max_len}")
+        longest = max(ends, default=0)
+        if max_kv is None:
+            max_kv = longest
+        if not longest <= max_kv <= self.max_len:
+            raise ValueError(f"max_kv must be {longest} to {self.max_len}, got {max_kv}")
         cu, pos, rows = [0], [], []
         for b, n in enumerate(new):
             cu.append(cu[-1] + n)
@@ -94,8 +113,8 @@ class AttentionBlock:
         self.lens[:len(new)] = ends
         dev = self.cache.device
         i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
-        return Plan(i32(cu), i32(ends), i32(pos), torch.tensor(rows, dtype=torch.int64, device=dev),
-                    max(new, default=0), max(ends, default=0) if max_kv is None else max_kv)
+        return Plan(self, new, i32(cu), i32(ends), i32(pos), torch.tensor(rows, dtype=torch.int64, device=dev),
+                    max(new, default=0), max_kv)
 
     def workspace(self, plan: Plan):
         """The attention workspace of a plan, for callers that keep it."""
@@ -109,6 +128,8 @@ class AttentionBlock:
         T, Hq, Hkv = plan.rows.numel(), self.Hq, self.Hkv
         if tuple(x.shape) != (T, self.hidden):
             raise ValueError(f"x must have shape {(T, self.hidden)}, got {tuple(x.shape)}")
+        if plan.longest > plan.max_kv:
+            raise ValueError(f"the plan was advanced to {plan.longest} tokens, its bound is {plan.max_kv}")
         qkv, o, y = self.qkv[:T], self.o[:T], self.y[:T]
         q, k = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv]
         A.fp8_linear(x, self.w_qkv, self.qkv_scale, y=qkv.view(T, -1), ws=self.ws)
@@ -195,12 +216,13 @@ def example(hidden=1024, q_heads=8, kv_heads=2, head_dim=128, n_experts=16, inte
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         x.copy_(block(x, step, ws))
-        step.advance()
+        step.advance()  # counts the first replay
     for t, v in zip((x, step.positions, step.kv_len, step.rows), start):
         t.copy_(v)
     for _ in range(steps):
         graph.replay()
         replayed.append(x.clone())
+    step.replayed(steps - 1)
     torch.cuda.synchronize()
     return eager, replayed
 

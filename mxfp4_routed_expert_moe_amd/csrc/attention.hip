@@ -847,7 +847,7 @@ int moe_attention(const moe_attn* a, void* ws, size_t ws_bytes, void* stream) {
   int st = moe::check_shape(a);
   if (st != MOE_OK) return st;
   if ((a->causal != 0 && a->causal != 1) || a->reserved != 0) return MOE_EINVAL;
-  if (!(a->scale > 0.f) || a->scale > 3.4e38f) return MOE_EINVAL;
+  if (!(a->scale > 0.f && a->scale <= 0x1p127f)) return MOE_EINVAL;  // scale * log2(e) is finite
   if ((a->kv_start == nullptr) != (a->kv_len == nullptr)) return MOE_EINVAL;
   if (a->n_seqs == 0 || a->q_rows == 0 || a->max_q == 0) return MOE_OK;
   if (!a->cu_q) return MOE_EINVAL;

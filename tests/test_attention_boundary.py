@@ -227,3 +227,7 @@ def test_fp8_linear_workspace_grows_with_every_size():
         assert got == sorted(got)
         for t in sizes:
             assert f(t, n, k) <= f(t, n + 1000 if n < 15000 else n, k) and f(t, n, k) <= f(t, n, min(k + 1600, 16384))
+
+
+def test_attention_scale_whose_base_two_form_overflows():
+    assert _attn(scale=2.0 ** 127 * 1.5) == EINVAL

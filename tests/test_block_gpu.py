@@ -124,3 +124,36 @@ def test_example_eager_and_graph():
     assert len(eager) == len(replayed) == 6
     for a, b in zip(eager, replayed):
         assert torch.isfinite(a.float()).all() and torch.equal(a, b)
+
+
+def test_a_plan_after_advances_and_their_bounds():
+    """What advances and replays brought counts for later plans; a plan stops at its bound, and a bound at the cache's room."""
+    b = _block(max_seqs=3, max_len=20, max_tokens=30)
+    print("[block] advances", flush=True)
+    prompt = b.plan([5, 0, 9])
+    b.forward(_x(14, 272, 1), prompt)
+    with pytest.raises(ValueError):
+        prompt.advance()
+    for bound in (9, 21):
+        with pytest.raises(ValueError):
+            b.plan([1, 0, 1], max_kv=bound)
+    assert b.lens == [5, 0, 9]
+    step = b.plan([1, 0, 1], max_kv=12)
+    for i in range(3):
+        b.forward(_x(2, 272, 2 + i), step)
+        step.advance()
+    with pytest.raises(ValueError):
+        b.forward(_x(2, 272, 5), step)
+    assert b.lens == [9, 0, 13] and step.kv_len.tolist() == [9, 3, 13]
+    b.lens[:] = [8, 0, 12]  # the step that was refused
+    late = b.plan([2, 4, 1])
+    x = _x(7, 272, 6)
+    b.forward(x, late)
+    assert late.positions.tolist() == [8, 9, 0, 1, 2, 3, 12] and late.kv_len.tolist() == [10, 4, 13]
+    seqs = [(0, 2, 0, 10), (2, 4, 20, 4), (6, 1, 40, 13)]
+    kv = _np(b.cache)
+    kv[10:20], kv[24:40], kv[53:] = 0, 0, 0
+    _check_attention(b.o[:7], None, _np(b.qkv[:7, :8]), kv[:, :2], kv[:, 2:], seqs, 64 ** -0.5, True)
+    one = b.plan([1], max_kv=20)
+    one.replayed(4)
+    assert b.lens[0] == 15 and one.longest == 15
