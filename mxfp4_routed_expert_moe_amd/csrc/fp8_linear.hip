@@ -292,12 +292,12 @@ __global__ __launch_bounds__(64 * kNW) void fp8_few_kernel(LinearArgs a) {
 // phase 2 b + 1.  The loads return in order, so a wait names how many of the
 // latest may still be out.
 //
-// With 256 x 256 tiles the steps are bound by the copies into LDS, 64 KB of them from
-// L2 per CU and step: 16384 x 6144 x 4096 takes 391 to 412 us with its 40 of
-// quantisation, 2.2 to 2.35 PFLOP/s for the product (a library product of quantised
-// operands with one scale each: 344 us), 4096^3 with float32 scales 79 to 84 with its 14, 2.0 to
-// 2.1 PFLOP/s (library: 54).  128 x 64 tiles with K split are bound by the latency of
-// a step, about 0.6 us.
+// With 256 x 256 tiles a phase takes about 1.7 times its products: 16384 x 6144 x 4096 in 386
+// to 397 us with its 40 of quantisation, 2.3 to 2.4 PFLOP/s for the product (a library
+// product of quantised operands with one scale each: 344 us); without the copies'
+// traffic, on zeros, the call would take 350.  4096^3 with float32 scales 80 to 82 with
+// its 14, 2.05 PFLOP/s (library: 54).  128 x 64 tiles with K split are bound by the
+// latency of a step, about 0.6 us.
 //
 // Layout: rows of 128 bytes, 16-byte chunk c of row r in slot c ^ ((r / 2) mod 8),
 // which spreads the 16 rows of a fragment read over all banks.  An operand's lane
@@ -360,26 +360,38 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(LinearArgs a) {
                           __builtin_amdgcn_readfirstlane(max(min(BN / 2, a.N - n0 - BN / 2), 0) * a.K)};
   const int x_rows = __builtin_amdgcn_readfirstlane(min(BT, a.T - t0));
   const int row0 = 8 * wave + (lane >> 3);
-  auto issue_w = [&](int h, uint8_t* to, int b) __attribute__((always_inline)) {
+  // Instruction i of the rows of group h, of block b.
+  auto issue_w = [&](int h, uint8_t* to, int b, int i) __attribute__((always_inline)) {
     int row = row0;
     asm volatile("" : "+v"(row));  // derived offsets are not kept in registers from step to step
     const __amdgpu_buffer_rsrc_t src =
         raw_buffer(a.w + static_cast<int64_t>(n0 + h * (BN / 2)) * a.K, b < end ? w_bytes[h] : 0);
     const int k = row * a.K + min(128 * b + 16 * slot(row, lane & 7), a.K - 16);
-#pragma unroll
-    for (int i = 0; i < kWOps; ++i) dma16(src, k + 64 * i * a.K, 0, to + 1024 * (8 * i + wave));
+    dma16(src, k + 64 * i * a.K, 0, to + 1024 * (8 * i + wave));
   };
+  // Instruction i of the tokens of block b; the last one takes their scales.
   const int spart = wave % (BT / 64);
-  auto issue_x = [&](Tokens& to, int b) __attribute__((always_inline)) {
-    int row = row0;
-    asm volatile("" : "+v"(row));
+  auto issue_x = [&](Tokens& to, int b, int i) __attribute__((always_inline)) {
     const int64_t first = static_cast<int64_t>(b) * a.T + t0;
     const int rows = b < end ? x_rows : 0;
-    const __amdgpu_buffer_rsrc_t src = raw_buffer(a.codes + 128 * first, 128 * rows);
-#pragma unroll
-    for (int i = 0; i < kXOps; ++i)
-      dma16(src, 128 * row + 16 * slot(row, lane & 7) + 8192 * i, 0, &to.x[1024 * (8 * i + wave)]);
-    dma4(raw_buffer(a.scales + first, 4 * rows), 4 * (64 * spart + lane), &to.s[64 * spart]);
+    if (i == kXOps) {
+      dma4(raw_buffer(a.scales + first, 4 * rows), 4 * (64 * spart + lane), &to.s[64 * spart]);
+      return;
+    }
+    int row = row0;
+    asm volatile("" : "+v"(row));
+    dma16(raw_buffer(a.codes + 128 * first, 128 * rows), 128 * row + 16 * slot(row, lane & 7) + 8192 * i, 0,
+          &to.x[1024 * (8 * i + wave)]);
+  };
+  // What an even phase issues for block b, and an odd one.
+  constexpr int kEven = kXOps + 1 + kWOps, kOdd = kWOps;
+  // Where they go out (us, first choice against the other): large tiles after the
+  // fragments are read (4096^3, float32 scales, 80.5 against 85.8; 768 x 6144 x 4096 38.8, 40.9) and
+  // between the products (16384 x 6144 x 4096 386 to 393, all at the start of them 405);
+  // 64 tokens, bound by latency, first of all (64 x 8192 x 8192 25.5, 26.9).
+  constexpr bool kLate = BT > 64, kSpread = BN == 256;
+  auto even_op = [&](Tokens& x, uint8_t* wb, int b, int i) __attribute__((always_inline)) {
+    if (i <= kXOps) issue_x(x, b, i); else issue_w(1, wb, b, i - kXOps - 1);
   };
 
   f32x4 acc[kN][kT];
@@ -406,7 +418,9 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(LinearArgs a) {
     for (int i = 0; i < kN; ++i) wf[i] = join(ld16(w + 2048 * i + c), ld16(w + 2048 * i + (c ^ 64)));
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto multiply = [&]() __attribute__((always_inline)) {
+  // The loads that go out in this phase can be spread over the products: a wave issues
+  // in order, and would wait for the queue of the loads before its first product.
+  auto multiply = [&](int ops, auto&& op) __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(1);
     float f[kT];
@@ -436,6 +450,10 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(LinearArgs a) {
                                                                      static_cast<int>(sw), 0, static_cast<int>(sx[j]));
       }
       __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < ops; ++k)
+        if ((kSpread ? k * kN * kT / ops : 0) == u) op(k);
+      __builtin_amdgcn_sched_barrier(0);
     }
     if (F32) {
 #pragma unroll
@@ -457,21 +475,21 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(LinearArgs a) {
     stage_barrier();
   };
 
-  issue_w(0, wa0, begin);
-  issue_x(x0, begin);
-  issue_w(1, wb0, begin);
-  issue_w(0, wa1, begin + 1);
+#pragma unroll
+  for (int i = 0; i < kOdd; ++i) issue_w(0, wa0, begin, i), issue_w(0, wa1, begin + 1, i);
+#pragma unroll
+  for (int i = 0; i < kEven; ++i) even_op(x0, wb0, begin, i);
   wait_vmcnt<0>();
   stage_barrier();
   int b = begin;
   if (group == 0) {
     auto step = [&](const Tokens& x, uint8_t* wa, Tokens& xn, uint8_t* wbn) __attribute__((always_inline)) {
-      issue_x(xn, b + 1);
-      issue_w(1, wbn, b + 1);
-      read(x, wa, b);
+      if (kLate) read(x, wa, b);
+#pragma unroll
+      for (int i = 0; i < kEven; ++i) even_op(xn, wbn, b + 1, i);
+      if (!kLate) read(x, wa, b);
       end_even();
-      issue_w(0, wa, b + 2);
-      multiply();
+      multiply(kOdd, [&](int i) __attribute__((always_inline)) { issue_w(0, wa, b + 2, i); });
       end_odd();
       ++b;
     };
@@ -481,23 +499,29 @@ __global__ __launch_bounds__(512, 2) void fp8_tile_kernel(LinearArgs a) {
     }
     if (b < end) step(x0, wa0, x1, wb1);
   } else {
-    auto step = [&](const Tokens& x, const uint8_t* wb, uint8_t* wa, Tokens& xn,
-                    uint8_t* wbn) __attribute__((always_inline)) {
-      issue_x(xn, b + 1);
-      issue_w(1, wbn, b + 1);
-      if (b > begin) multiply();
+    auto odd = [&](const Tokens& x, const uint8_t* wb, uint8_t* wa) __attribute__((always_inline)) {
       end_even();
-      issue_w(0, wa, b + 2);
-      read(x, wb, b);
+      if (kLate) read(x, wb, b);
+#pragma unroll
+      for (int i = 0; i < kOdd; ++i) issue_w(0, wa, b + 2, i);
+      if (!kLate) read(x, wb, b);
       end_odd();
       ++b;
     };
+    auto step = [&](const Tokens& x, const uint8_t* wb, uint8_t* wa, Tokens& xn,
+                    uint8_t* wbn) __attribute__((always_inline)) {
+      multiply(kEven, [&](int i) __attribute__((always_inline)) { even_op(xn, wbn, b + 1, i); });
+      odd(x, wb, wa);
+    };
+#pragma unroll
+    for (int i = 0; i < kEven; ++i) even_op(x1, wb1, b + 1, i);
+    odd(x0, wb0, wa0);
     while (b + 1 < end) {
-      step(x0, wb0, wa0, x1, wb1);
       step(x1, wb1, wa1, x0, wb0);
+      step(x0, wb0, wa0, x1, wb1);
     }
-    if (b < end) step(x0, wb0, wa0, x1, wb1);
-    multiply();
+    if (b < end) step(x1, wb1, wa1, x0, wb0);
+    multiply(0, [](int) {});
   }
   wait_vmcnt<0>();  // no DMA is left for the LDS of the next block
 
