@@ -32,6 +32,7 @@
 #include <algorithm>
 
 #include "../../include/moe_attention.h"
+#include "attention_ranges.h"
 #include "lds_dma.h"
 #include "moe_internal.h"
 
@@ -267,16 +268,8 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // lq keeps the full length (the causal diagonal hangs on it); only the rows
 // below max_q are worked on.
 __device__ __forceinline__ void sequence(const AttnArgs& a, int b, int& q0, int& lq, int& k0, int& lk) {
-  q0 = min(max(a.cu_q[b], 0), a.q_rows);
-  lq = max(min(a.cu_q[b + 1], a.q_rows) - q0, 0);
-  if (a.kv_start) {
-    k0 = min(max(a.kv_start[b], 0), a.kv_rows);
-    lk = max(min(a.kv_len[b], a.kv_rows - k0), 0);
-  } else {
-    k0 = min(q0, a.kv_rows);
-    lk = min(lq, a.kv_rows - k0);
-  }
-  lk = min(lk, a.max_kv);
+  const SeqRange s = seq_range(a.cu_q, a.kv_start, a.kv_len, b, a.q_rows, a.kv_rows, a.max_kv);
+  q0 = s.q0, lq = s.lq, k0 = s.k0, lk = s.lk;
 }
 __device__ __forceinline__ int row_tiles(const AttnArgs& a, int lq, int rows) {
   return (min(lq, a.max_q) * a.group + rows - 1) / rows;

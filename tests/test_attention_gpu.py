@@ -573,3 +573,25 @@ def test_fp8_linear_tiles_and_splits(T, N, K, kind):
     rows = np.unique(np.r_[0, T - 1, g.integers(0, T, 40)])
     ref, mag, top = R.fp8_linear(x[rows], codes, sv, kind)
     _check_linear(y[torch.from_numpy(rows).cuda()], ref, mag, top, K)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("G,D", [(1, 64), (40, 128)])
+def test_attention_row_ends_below_every_row(G, D, causal):
+    """cu_q entries far below zero, in the middle and at the end, behind a sequence that begins above row 0: that sequence
+    is empty, and nothing outside q's rows is written."""
+    _say("attention row ends", G, D, causal)
+    g = np.random.default_rng(16)
+    T, lead = 40, 8
+    q = R.bf16(g.normal(0, 1, (T, G, D)))
+    k, v = R.bf16(g.normal(0, 1, (T, 1, D))), R.bf16(g.normal(0, 1, (T, 1, D)))
+    low = -(1 << 31)
+    out = torch.full((lead + T + lead, G, D), 9.0, dtype=BF, device="cuda")
+    lse = torch.full((lead + T + lead, G), 3.0, device="cuda")
+    cu = torch.tensor([5, low, 10, low + 3, 20, 31, low + 1], dtype=torch.int32, device="cuda")
+    A.attention(_bf16(q), _bf16(k), _bf16(v), cu, T, causal=causal, out=out[lead:lead + T], lse=lse[lead:lead + T])
+    # the entries low begin at row 0 (rows 0 to 9 are named twice); rows 20 to 30 belong to one sequence, rows from 31 on to none
+    seqs = [(20, 11, 20, 11)]
+    _check_attention(out[lead:lead + T], lse[lead:lead + T], q, k, v, seqs, D ** -0.5, causal)
+    assert torch.all(out[:lead] == 9) and torch.all(out[lead + 31:] == 9)
+    assert torch.all(lse[:lead] == 3) and torch.all(lse[lead + 31:] == 3)
