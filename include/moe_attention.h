@@ -131,7 +131,9 @@ int moe_qk_norm_rope(const moe_heads* q, int32_t q_heads, const moe_heads* k, in
  * no value in them reads or writes outside the tensors; rows of out and lse that belong to no
  * sequence are left as they are.  max_q and max_kv are the caller's bounds on
  * Lq and Lk (host values; they choose kernels, grids and splits): rows of a
- * sequence past max_q get no output, keys past max_kv are not seen.
+ * sequence past max_q get no output, keys past max_kv are not seen.  Bounds and cuts
+ * of the keys take keys away and move nothing: Lk above is kv_len[b] (Lq) as given,
+ * Lq the length that cu_q gives inside q's rows.
  *
  * The struct is a host object, read during the call.
  */

@@ -258,18 +258,16 @@ __device__ __forceinline__ void attend_masked(const uint8_t* ks, const uint8_t* 
 
 // ---------------------------------------------------------------- work
 // A tile of up to `rows` folded rows of one sequence.  All fields are uniform.
-struct TileWork {
-  int q0, lq, k0, lk, tile, tiles;
+struct TileWork : SeqRange {
+  int tile, tiles;
 };
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// Rows and keys of sequence b, cut to the tensors and to the caller's bounds.
-// lq keeps the full length (the causal diagonal hangs on it); only the rows
-// below max_q are worked on.
-__device__ __forceinline__ void sequence(const AttnArgs& a, int b, int& q0, int& lq, int& k0, int& lk) {
-  const SeqRange s = seq_range(a.cu_q, a.kv_start, a.kv_len, b, a.q_rows, a.kv_rows, a.max_kv);
-  q0 = s.q0, lq = s.lq, k0 = s.k0, lk = s.lk;
+// Rows and keys of sequence b, cut to the tensors and to max_kv.  lq keeps the
+// full length; only the rows below max_q are worked on.
+__device__ __forceinline__ SeqRange sequence(const AttnArgs& a, int b) {
+  return seq_range(a.cu_q, a.kv_start, a.kv_len, b, a.q_rows, a.kv_rows, a.max_kv);
 }
 __device__ __forceinline__ int row_tiles(const AttnArgs& a, int lq, int rows) {
   return (min(lq, a.max_q) * a.group + rows - 1) / rows;
@@ -280,19 +278,21 @@ __device__ __forceinline__ int row_tiles(const AttnArgs& a, int lq, int rows) {
 __device__ bool find_tile(const AttnArgs& a, int t, int rows, TileWork& w) {
   const int lane = threadIdx.x & 63;
   for (int base = 0; base < a.n_seqs; base += 64) {
-    int q0 = 0, lq = 0, k0 = 0, lk = 0, nt = 0;
+    SeqRange s = {0, 0, 0, 0, 0};
+    int nt = 0;
     if (base + lane < a.n_seqs) {
-      sequence(a, base + lane, q0, lq, k0, lk);
-      nt = row_tiles(a, lq, rows);
+      s = sequence(a, base + lane);
+      nt = row_tiles(a, s.lq, rows);
     }
     const int incl = wave_incl_scan(nt);
     const uint64_t past = __ballot(incl > t);
     if (past) {
       const int src = __ffsll(static_cast<unsigned long long>(past)) - 1;
-      w.q0 = uniform(__shfl(q0, src, 64));
-      w.lq = uniform(__shfl(lq, src, 64));
-      w.k0 = uniform(__shfl(k0, src, 64));
-      w.lk = uniform(__shfl(lk, src, 64));
+      w.q0 = uniform(__shfl(s.q0, src, 64));
+      w.lq = uniform(__shfl(s.lq, src, 64));
+      w.k0 = uniform(__shfl(s.k0, src, 64));
+      w.lk = uniform(__shfl(s.lk, src, 64));
+      w.diag = uniform(__shfl(s.diag, src, 64));
       w.tiles = uniform(__shfl(nt, src, 64));
       w.tile = uniform(t - (__shfl(incl, src, 64) - w.tiles));
       return true;
@@ -302,9 +302,8 @@ __device__ bool find_tile(const AttnArgs& a, int t, int rows, TileWork& w) {
   return false;
 }
 
-// The last key that query `pos` sees (-1 or less: none).
 __device__ __forceinline__ int last_key(const AttnArgs& a, const TileWork& w, int pos) {
-  return a.causal ? min(pos + w.lk - w.lq, w.lk - 1) : w.lk - 1;
+  return last_key(static_cast<const SeqRange&>(w), a.causal, pos);
 }
 
 // A lane's row: the query row and head it reads and writes.
@@ -507,8 +506,9 @@ __global__ __launch_bounds__(64 * decode_waves<D>(), 1) void attn_token_kernel(A
   // elsewhere (64 x up to 8192 keys: 237 us against 246).
   const int kv_head = (blockIdx.x + seq + split) % a.kv_heads;
   TileWork w;
-  sequence(a, seq, w.q0, w.lq, w.k0, w.lk);
-  w.q0 = uniform(w.q0), w.lq = uniform(w.lq), w.k0 = uniform(w.k0), w.lk = uniform(w.lk);
+  const SeqRange range = sequence(a, seq);
+  w.q0 = uniform(range.q0), w.lq = uniform(range.lq), w.k0 = uniform(range.k0), w.lk = uniform(range.lk);
+  w.diag = uniform(range.diag);
   const int n_rows = min(w.lq, a.max_q) * a.group;
   if (n_rows == 0) return;
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -633,7 +633,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   if (a.token) {  // u counts the rows below max_q of each sequence
     const int seq = static_cast<int>(q_row / a.max_q);
     if (seq >= a.n_seqs) return;
-    sequence(a, seq, w.q0, w.lq, w.k0, w.lk);
+    static_cast<SeqRange&>(w) = sequence(a, seq);
     pos = static_cast<int>(q_row - static_cast<int64_t>(seq) * a.max_q);
     q_row = w.q0 + pos;
   } else {  // u counts q's rows: the sequence is the last one that begins at or before it
@@ -643,7 +643,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
       const int mid = (lo + hi) / 2;
       if (a.cu_q[mid] <= q_row) lo = mid; else hi = mid;
     }
-    sequence(a, lo, w.q0, w.lq, w.k0, w.lk);
+    static_cast<SeqRange&>(w) = sequence(a, lo);
     pos = static_cast<int>(q_row) - w.q0;
   }
   if (pos < 0 || pos >= min(w.lq, a.max_q)) return;

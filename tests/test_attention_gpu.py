@@ -595,3 +595,34 @@ def test_attention_row_ends_below_every_row(G, D, causal):
     _check_attention(out[lead:lead + T], lse[lead:lead + T], q, k, v, seqs, D ** -0.5, causal)
     assert torch.all(out[:lead] == 9) and torch.all(out[lead + 31:] == 9)
     assert torch.all(lse[:lead] == 3) and torch.all(lse[lead + 31:] == 3)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lq,lk,rows,max_q,max_kv,Hq,Hkv,D", [
+    # prompts longer than max_q; k of fewer rows than q
+    (40, None, 40, 25, 40, 2, 2, 64), (40, None, 40, 25, 40, 8, 2, 128), (300, None, 300, 130, 300, 2, 1, 256),
+    (40, None, 30, 40, 30, 4, 2, 128), (9, None, 5, 9, 5, 2, 2, 64),
+    # chunks: keys past max_kv, rows past max_q, both; caches that end inside the sequence
+    (40, 100, 100, 40, 60, 4, 2, 128), (10, 100, 100, 10, 60, 4, 2, 64), (40, 100, 100, 7, 60, 4, 2, 256),
+    (40, 100, 70, 40, 70, 2, 1, 64), (6, 90, 70, 6, 70, 8, 2, 128),
+    # the same, split and joined
+    (50, 9000, 9000, 50, 6000, 2, 1, 64), (50, 9000, 9000, 30, 8960, 4, 1, 128), (6, 9000, 9000, 6, 8000, 4, 1, 128),
+    (12, 9000, 9000, 3, 8999, 16, 2, 256), (40, 6000, 5990, 40, 5990, 2, 1, 256)])
+def test_attention_cuts_leave_the_diagonal(lq, lk, rows, max_q, max_kv, Hq, Hkv, D, causal):
+    """Rows past max_q get no output and keys past max_kv or past the end of k are not seen; what the other rows see of the
+    other keys is what they see without the cut."""
+    _say("attention cuts", lq, lk, rows, max_q, max_kv, Hq, Hkv, D, causal)
+    g = np.random.default_rng(lq + max_q + max_kv)
+    q = R.bf16(g.normal(0, 2, (lq, Hq, D)))
+    k, v = R.bf16(g.normal(0, 1, (rows, Hkv, D))), R.bf16(g.normal(0, 1, (rows, Hkv, D)))
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = torch.full((lq, Hq, D), 9.0, dtype=BF, device="cuda")
+    lse = torch.full((lq, Hq), 3.0, device="cuda")
+    kw = dict(kv_start=i32([0]), kv_len=i32([lk])) if lk else {}
+    A.attention(_bf16(q), _bf16(k), _bf16(v), i32([0, lq]), max_q, max_kv=max_kv, causal=causal, out=out, lse=lse, **kw)
+    n = lk or lq
+    there = min(n, rows, max_kv)
+    # row by row: as many keys as the formula leaves of those that are there
+    seqs = [(i, 1, 0, min(max(i + n - lq + 1, 0), there) if causal else there) for i in range(max_q)]
+    _check_attention(out, lse, q, k, v, seqs, D ** -0.5, False)
+    assert torch.all(out[max_q:] == 9) and torch.all(lse[max_q:] == 3)

@@ -23,6 +23,10 @@ extern "C" void ranges(const int32_t* cu_q, const int32_t* kv_start, const int32
     out[4 * b] = s.q0, out[4 * b + 1] = s.lq, out[4 * b + 2] = s.k0, out[4 * b + 3] = s.lk;
   }
 }
+extern "C" int last(const int32_t* cu_q, const int32_t* kv_start, const int32_t* kv_len, int q_rows, int kv_rows,
+                    int max_kv, int causal, int pos) {
+  return moe::last_key(moe::seq_range(cu_q, kv_start, kv_len, 0, q_rows, kv_rows, max_kv), causal, pos);
+}
 """
 
 
@@ -63,3 +67,18 @@ def test_every_value_stays_inside_the_tensors(lib, q_rows, kv_rows, max_kv):
         assert np.array_equal(q0, a) and np.array_equal(lq, np.maximum(b - a, 0))
         assert np.all(q0 >= 0) and np.all(q0 + lq <= q_rows)
         assert np.all(k0 >= 0) and np.all(lk >= 0) and np.all(k0 + lk <= kv_rows) and np.all(lk <= max_kv)
+
+
+@pytest.mark.parametrize("cache", [False, True])
+def test_last_key_hangs_on_the_lengths_as_given(lib, cache):
+    """Key j is seen where j <= i + Lk - Lq (causal) and where it is there: inside Lk, k's rows and max_kv."""
+    p = lambda v: np.asarray(v, np.int32).ctypes.data_as(ctypes.c_void_p)  # noqa: E731
+    for lq, lk, k0, kv_rows, max_kv in itertools.product((1, 5, 9), (0, 1, 5, 7, 12, HIGH), (0, 3), (0, 4, 20), (0, 3, 6, 20)):
+        if not cache:
+            lk, k0 = lq, 2
+        for causal, i in itertools.product((0, 1), range(lq)):
+            got = lib.last(p([2, 2 + lq]), p([k0]) if cache else None, p([lk]) if cache else None, 2 + lq, kv_rows, max_kv,
+                           causal, i)
+            there = min(lk, max(kv_rows - k0, 0), max_kv)
+            seen = [j for j in range(there) if not causal or j <= i + lk - lq]
+            assert max(got, -1) == max(seen, default=-1), (lq, lk, k0, kv_rows, max_kv, causal, i)
