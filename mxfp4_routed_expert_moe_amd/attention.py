@@ -253,7 +253,9 @@ def attention(q, k, v, cu_q, max_q: int, *, kv_start=None, kv_len=None, max_kv=N
     any row and head strides (multiples of 8) -> out [q_rows, Hq, D].
 
     cu_q int32 [B + 1]: the rows of q of each sequence; max_q (and max_kv): the
-    caller's bounds on their lengths.  Without kv_start and kv_len the keys of
+    caller's bounds on their lengths.  max_kv None: every key (a call over a cache, or
+    over several prompts that is not causal, is split better where max_kv names the longest
+    sequence; a workspace is for the bound that was given).  Without kv_start and kv_len the keys of
     a sequence are the rows that cu_q names; with them (int32 [B]) they are
     rows kv_start[b] .. kv_start[b] + kv_len[b] - 1 of a cache, the new rows included.
     scale: default D ** -0.5.  lse: float32 [q_rows, Hq] to fill, or None.  Rows
@@ -282,8 +284,8 @@ def attention(q, k, v, cu_q, max_q: int, *, kv_start=None, kv_len=None, max_kv=N
     if out is None:
         out = torch.empty(qshape, dtype=torch.bfloat16, device=q.device)
     ho = _heads(out, "out", dev, qshape)
-    if max_kv is None:
-        max_kv = Tk if start else min(max_q, Tk)
+    if max_kv is None:  # no row below max_q of a causal prompt sees a key from max_q on
+        max_kv = min(max_q, Tk) if causal and not start else Tk
     a = _ATTN.pack(B.MOE_ABI_VERSION, D, Hq, Hk, n_seqs, Tq, Tk, max_q, max_kv, 1 if causal else 0,
                    D ** -0.5 if scale is None else scale, 0, *hq, *hk, *hv, *ho, cu, start, length, lp)
     L = lib()

@@ -626,3 +626,24 @@ def test_attention_cuts_leave_the_diagonal(lq, lk, rows, max_q, max_kv, Hq, Hkv,
     seqs = [(i, 1, 0, min(max(i + n - lq + 1, 0), there) if causal else there) for i in range(max_q)]
     _check_attention(out, lse, q, k, v, seqs, D ** -0.5, False)
     assert torch.all(out[max_q:] == 9) and torch.all(lse[max_q:] == 3)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lq,max_q,Hq,Hkv,D", [([40], 25, 2, 2, 64), ([40], 25, 8, 2, 128), ([300, 90], 130, 2, 1, 256),
+                                               ([3, 0, 50], 4, 4, 2, 64)])
+def test_attention_prompts_past_max_q_without_max_kv(lq, max_q, Hq, Hkv, D, causal):
+    """The rows below max_q see every key that the formula gives them, whatever max_q."""
+    _say("attention prompts past max_q", lq, max_q, Hq, Hkv, D, causal)
+    g = np.random.default_rng(sum(lq) + max_q)
+    T = sum(lq)
+    q = R.bf16(g.normal(0, 2, (T, Hq, D)))
+    k, v = R.bf16(g.normal(0, 1, (T, Hkv, D))), R.bf16(g.normal(0, 1, (T, Hkv, D)))
+    q0, seqs = _seqs(lq)
+    out = torch.full((T, Hq, D), 9.0, dtype=BF, device="cuda")
+    lse = torch.full((T, Hq), 3.0, device="cuda")
+    A.attention(_bf16(q), _bf16(k), _bf16(v), torch.tensor(q0, dtype=torch.int32, device="cuda"), max_q, causal=causal,
+                out=out, lse=lse)
+    rows = [(a + i, 1, a, i + 1 if causal else n) for a, n, _, _ in seqs for i in range(min(n, max_q))]
+    _check_attention(out, lse, q, k, v, rows, D ** -0.5, False)
+    for a, n, _, _ in seqs:
+        assert torch.all(out[a + max_q:a + n] == 9) and torch.all(lse[a + max_q:a + n] == 3)
