@@ -27,31 +27,55 @@ class Plan:
 
     cu_q, kv_len, positions and rows are int32 (rows: int64) device tensors;
     max_q and max_kv bound the sequences' new tokens and cached lengths.  The
-    block that made the plan knows how many tokens each sequence holds; advance
-    and replayed keep that in step."""
+    block that made the plan knows how many tokens each sequence holds; forward,
+    advance and replayed keep that in step."""
 
-    def __init__(self, block, new, cu_q, kv_len, positions, rows, max_q, max_kv):
-        self.block, self.new = block, list(new)
+    def __init__(self, block, number, new, cu_q, kv_len, positions, rows, max_q, max_kv, longest):
+        self.block, self.number, self.new = block, number, list(new)
         self.cu_q, self.kv_len, self.positions, self.rows = cu_q, kv_len, positions, rows
         self.max_q, self.max_kv = max_q, max_kv
-        self.longest = max(block.lens[:len(self.new)], default=0)
+        self.steps = 0  # how often it was advanced
+        self.longest = longest  # of the sequences, with the plan's tokens
 
     def advance(self):
         """The same call one token later (plans of at most one token per
-        sequence): three additions on the current stream.  The last step is the
-        one whose longest sequence holds max_kv tokens."""
+        sequence): three additions on the current stream.  The step before counts
+        as run; the one that is announced counts for later plans once it has
+        run, by forward, or by the next advance after a graph's replay.  The last
+        step is the one whose longest sequence holds max_kv tokens."""
         self.replayed(1)
+        self._shift()
+
+    def _shift(self):
+        """The device's part of advance."""
         self.positions.add_(1)
         self.kv_len.add_(1)
         self.rows.add_(1)
 
     def replayed(self, steps: int):
-        """Note `steps` replays of a HIP graph that holds advance()."""
+        """Note `steps` replays of a HIP graph that holds forward and then advance()."""
         if any(n > 1 for n in self.new):
             raise ValueError("a plan of more than one token per sequence cannot be advanced")
-        for b, n in enumerate(self.new):
-            self.block.lens[b] += n * steps
+        if steps < 0:
+            raise ValueError(f"steps must not be negative, got {steps}")
+        self._check_place()
+        if steps == 0:
+            return
+        for b in self._sequences():
+            self.block.lens[b] += steps
+            self.block._announced[b] = self.block.lens[b]
+        self.steps += steps
         self.longest += steps
+
+    def _sequences(self):
+        """The sequences that the plan brings tokens to."""
+        return [b for b, n in enumerate(self.new) if n]
+
+    def _check_place(self):
+        """The next token of a sequence is this plan's to bring until a later plan brings one."""
+        for b in self._sequences():
+            if self.block._owner[b] != self.number:
+                raise ValueError(f"a later plan has brought tokens to sequence {b}: make a new plan")
 
 
 class AttentionBlock:
@@ -79,7 +103,10 @@ class AttentionBlock:
         self.rope = dict(rot_offset=rot_offset, interleaved=interleaved, eps=eps)
         self.max_seqs, self.max_len, self.max_tokens = max_seqs, max_len, max_tokens
         dev, bf16 = w_qkv.device, torch.bfloat16
-        self.lens = [0] * max_seqs  # tokens that each sequence holds once its plans have run
+        self.lens = [0] * max_seqs  # tokens that each sequence holds once its plans and their announced steps have run
+        self._announced = [None] * max_seqs  # what lens is with a step that was announced and has not run
+        self._owner = [0] * max_seqs  # the number of the last plan that brought tokens
+        self._plans = 0
         self.cache = torch.empty((max_seqs * max_len, 2 * kv_heads, head_dim), dtype=bf16, device=dev)
         self.kv_start = torch.arange(0, max_seqs * max_len, max_len, dtype=torch.int32, device=dev)
         self.qkv = torch.empty((max_tokens, q_heads + 2 * kv_heads, head_dim), dtype=bf16, device=dev)
@@ -88,16 +115,22 @@ class AttentionBlock:
         self.ws = A.fp8_linear_workspace(max_tokens, max(w_qkv.shape[0], self.hidden),
                                          max(self.hidden, w_out.shape[1]), dev)
 
+    def held(self, b: int) -> int:
+        """Tokens of sequence b that count for the next plan: those of all plans made so
+        far, and of the steps of advanced plans that have run."""
+        return self.lens[b] - (self._announced[b] == self.lens[b])
+
     def plan(self, new, max_kv=None) -> Plan:
-        """A call that brings new[b] tokens to sequence b, after those that earlier
-        plans and their advances brought (host list; fewer entries than max_seqs: the
-        first ones).  max_kv: the bound on the cached lengths, this call's by
+        """A call that brings new[b] tokens to sequence b, after those it holds (host
+        list; fewer entries than max_seqs: the first ones).  Plans run in the order in
+        which they were made.  max_kv: the bound on the cached lengths, this call's by
         default; a plan that is to be advanced passes the one of its last step."""
         if len(new) > self.max_seqs or any(n < 0 for n in new):
             raise ValueError(f"new must hold up to {self.max_seqs} counts")
         if sum(new) > self.max_tokens:
             raise ValueError(f"{sum(new)} tokens, the block was built for {self.max_tokens}")
-        ends = [have + n for have, n in zip(self.lens, new)]
+        held = [self.held(b) for b in range(len(new))]
+        ends = [have + n for have, n in zip(held, new)]
         if any(e > self.max_len for e in ends):
             raise ValueError(f"a sequence would hold {max(ends)} tokens, the cache has room for {self.max_len}")
         longest = max(ends, default=0)
@@ -108,13 +141,16 @@ class AttentionBlock:
         cu, pos, rows = [0], [], []
         for b, n in enumerate(new):
             cu.append(cu[-1] + n)
-            pos.extend(range(self.lens[b], ends[b]))
-            rows.extend(range(b * self.max_len + self.lens[b], b * self.max_len + ends[b]))
-        self.lens[:len(new)] = ends
+            pos.extend(range(held[b], ends[b]))
+            rows.extend(range(b * self.max_len + held[b], b * self.max_len + ends[b]))
+        self._plans += 1
+        for b, n in enumerate(new):
+            if n:  # an announced step of a sequence without new tokens keeps its place
+                self.lens[b], self._announced[b], self._owner[b] = ends[b], None, self._plans
         dev = self.cache.device
         i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
-        return Plan(self, new, i32(cu), i32(ends), i32(pos), torch.tensor(rows, dtype=torch.int64, device=dev),
-                    max(new, default=0), max_kv)
+        return Plan(self, self._plans, new, i32(cu), i32(ends), i32(pos), torch.tensor(rows, dtype=torch.int64, device=dev),
+                    max(new, default=0), max_kv, longest)
 
     def workspace(self, plan: Plan):
         """The attention workspace of a plan, for callers that keep it."""
@@ -125,11 +161,22 @@ class AttentionBlock:
     def forward(self, x, plan: Plan, ws=None):
         """x bf16 [tokens of the plan, hidden] -> y of the same shape, a view of
         the block's buffer (valid until its next call)."""
-        T, Hq, Hkv = plan.rows.numel(), self.Hq, self.Hkv
+        T = plan.rows.numel()
         if tuple(x.shape) != (T, self.hidden):
             raise ValueError(f"x must have shape {(T, self.hidden)}, got {tuple(x.shape)}")
         if plan.longest > plan.max_kv:
             raise ValueError(f"the plan was advanced to {plan.longest} tokens, its bound is {plan.max_kv}")
+        if plan.steps:
+            plan._check_place()
+        y = self._enqueue(x, plan, ws)
+        for b in plan._sequences():
+            if self._owner[b] == plan.number:
+                self._announced[b] = None
+        return y
+
+    def _enqueue(self, x, plan: Plan, ws):
+        """The device's part of forward."""
+        T, Hq, Hkv = plan.rows.numel(), self.Hq, self.Hkv
         qkv, o, y = self.qkv[:T], self.o[:T], self.y[:T]
         q, k = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv]
         A.fp8_linear(x, self.w_qkv, self.qkv_scale, y=qkv.view(T, -1), ws=self.ws)
@@ -219,10 +266,10 @@ def example(hidden=1024, q_heads=8, kv_heads=2, head_dim=128, n_experts=16, inte
         step.advance()  # counts the first replay
     for t, v in zip((x, step.positions, step.kv_len, step.rows), start):
         t.copy_(v)
+    step.replayed(steps - 1)
     for _ in range(steps):
         graph.replay()
         replayed.append(x.clone())
-    step.replayed(steps - 1)
     torch.cuda.synchronize()
     return eager, replayed
 

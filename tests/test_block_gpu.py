@@ -157,3 +157,46 @@ def test_a_plan_after_advances_and_their_bounds():
     one = b.plan([1], max_kv=20)
     one.replayed(4)
     assert b.lens[0] == 15 and one.longest == 15
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_chunks_after_the_step_loop(graph):
+    """forward, advance, forward, advance, ... eager or as a graph of both, then a chunk: its attention is that of the
+    reference over every token that ran, and over no row that none wrote."""
+    b = _block(max_seqs=3, max_len=40, max_tokens=30)
+    print("[block] chunk after the loop", graph, flush=True)
+    b.cache.fill_(float("nan"))
+    b.forward(_x(14, 272, 1), b.plan([5, 0, 9]))
+    step = b.plan([1, 0, 1], max_kv=30)
+    x = _x(2, 272, 2)
+    if graph:
+        start = [t.clone() for t in (step.positions, step.kv_len, step.rows)]
+        ws = b.workspace(step)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            b.forward(x, step, ws)
+        torch.cuda.current_stream().wait_stream(side)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            b.forward(x, step, ws)
+            step.advance()
+        for t, v in zip((step.positions, step.kv_len, step.rows), start):
+            t.copy_(v)
+        step.replayed(3)
+        for _ in range(4):
+            g.replay()
+    else:
+        for _ in range(4):
+            b.forward(x, step)
+            step.advance()
+    torch.cuda.synchronize()
+    assert [b.held(s) for s in range(3)] == [9, 0, 13]
+    late = b.plan([2, 4, 1])
+    b.forward(_x(7, 272, 6), late)
+    assert late.positions.tolist() == [9, 10, 0, 1, 2, 3, 13] and late.kv_len.tolist() == [11, 4, 14]
+    kv = _np(b.cache)
+    for s, n in enumerate((11, 4, 14)):
+        assert np.isfinite(kv[40 * s:40 * s + n]).all() and np.isnan(kv[40 * s + n:40 * s + 40]).all()
+    seqs = [(0, 2, 0, 11), (2, 4, 40, 4), (6, 1, 80, 14)]
+    _check_attention(b.o[:7], None, _np(b.qkv[:7, :8]), np.nan_to_num(kv[:, :2]), np.nan_to_num(kv[:, 2:]), seqs, 64 ** -0.5, True)
