@@ -120,6 +120,14 @@ class AttentionBlock:
         far, and of the steps of advanced plans that have run."""
         return self.lens[b] - (self._announced[b] == self.lens[b])
 
+    def reset(self, b=None):
+        """Forget the tokens of sequence b (None: of all): its next plan begins at position 0."""
+        if b is not None and not 0 <= b < self.max_seqs:
+            raise ValueError(f"there are {self.max_seqs} sequences, got {b}")
+        self._plans += 1  # no earlier plan can be advanced there
+        for s in range(self.max_seqs) if b is None else (b,):
+            self.lens[s], self._announced[s], self._owner[s] = 0, None, self._plans
+
     def plan(self, new, max_kv=None) -> Plan:
         """A call that brings new[b] tokens to sequence b, after those it holds (host
         list; fewer entries than max_seqs: the first ones).  Plans run in the order in

@@ -158,3 +158,40 @@ def test_a_graph_of_forward_alone(model):
         model.check([1])
         step.advance()
     model.run([2])
+
+
+def test_a_full_sequence_and_its_slot(model):
+    """A sequence filled to the cache's end by a loop that ends with an advance: plans beside it go on, more tokens for it
+    are refused, and reset makes its slot free for another sequence."""
+    model.run([18, 2])
+    step = model.b.plan([1], max_kv=20)
+    for _ in range(2):
+        model.run([1], step)
+        step.advance()
+    with pytest.raises(ValueError):
+        model.b.forward(torch.zeros(1, HIDDEN).bfloat16(), step)
+    model.run([0, 3])
+    with pytest.raises(ValueError):
+        model.b.plan([1])
+    model.b.reset(0)
+    model.fed[0] = []
+    with pytest.raises(ValueError):
+        step.advance()
+    model.run([4, 1])
+    model.b.reset()
+    model.fed = [[], [], []]
+    model.run([1, 2, 20])
+    for bad in (-1, 3):
+        with pytest.raises(ValueError):
+            model.b.reset(bad)
+
+
+def test_reset_of_a_sequence_with_an_announced_step(model):
+    model.run([3, 4])
+    step = model.run([1, 1], max_kv=20)
+    step.advance()
+    model.b.reset(1)
+    model.fed[1] = []
+    with pytest.raises(ValueError):
+        model.b.forward(torch.zeros(2, HIDDEN).bfloat16(), step)
+    model.run([2, 2])
