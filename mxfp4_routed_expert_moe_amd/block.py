@@ -35,7 +35,7 @@ class Plan:
         self.cu_q, self.kv_len, self.positions, self.rows = cu_q, kv_len, positions, rows
         self.max_q, self.max_kv = max_q, max_kv
         self.steps = 0  # how often it was advanced
-        self.longest = longest  # of the sequences, with the plan's tokens
+        self.longest = longest  # of its sequences, with the plan's tokens
 
     def advance(self):
         """The same call one token later (plans of at most one token per
@@ -131,8 +131,8 @@ class AttentionBlock:
     def plan(self, new, max_kv=None) -> Plan:
         """A call that brings new[b] tokens to sequence b, after those it holds (host
         list; fewer entries than max_seqs: the first ones).  Plans run in the order in
-        which they were made.  max_kv: the bound on the cached lengths, this call's by
-        default; a plan that is to be advanced passes the one of its last step."""
+        which they were made.  max_kv: the bound on the cached lengths of the sequences
+        that get tokens, this call's by default; a plan that is to be advanced passes the one of its last step."""
         if len(new) > self.max_seqs or any(n < 0 for n in new):
             raise ValueError(f"new must hold up to {self.max_seqs} counts")
         if sum(new) > self.max_tokens:
@@ -141,7 +141,7 @@ class AttentionBlock:
         ends = [have + n for have, n in zip(held, new)]
         if any(e > self.max_len for e in ends):
             raise ValueError(f"a sequence would hold {max(ends)} tokens, the cache has room for {self.max_len}")
-        longest = max(ends, default=0)
+        longest = max((e for e, n in zip(ends, new) if n), default=0)
         if max_kv is None:
             max_kv = longest
         if not longest <= max_kv <= self.max_len:

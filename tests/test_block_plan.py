@@ -195,3 +195,22 @@ def test_reset_of_a_sequence_with_an_announced_step(model):
     with pytest.raises(ValueError):
         model.b.forward(torch.zeros(2, HIDDEN).bfloat16(), step)
     model.run([2, 2])
+
+
+@pytest.mark.parametrize("lens", [[15, 5], [20, 0]])
+def test_a_long_idle_sequence_does_not_bound_the_others(model, lens):
+    """max_kv bounds the sequences that a plan brings tokens to; an idle one beside them may be longer, or full."""
+    model.run(lens)
+    bound = lens[1] + 3
+    with pytest.raises(ValueError):
+        model.b.plan([0, 1], max_kv=lens[1])
+    step = model.b.plan([0, 1], max_kv=bound)
+    for _ in range(3):
+        model.run([0, 1], step)
+        assert model.calls[-1][-1] == bound
+        step.advance()
+    with pytest.raises(ValueError):
+        model.b.forward(torch.zeros(1, HIDDEN).bfloat16(), step)
+    plan = model.b.plan([0, 2])
+    assert plan.max_kv == lens[1] + 5
+    model.run([0, 2], plan)
