@@ -25,21 +25,23 @@ from . import attention as A
 class Plan:
     """The tokens of one call, sequence after sequence, and where they go.
 
-    cu_q, kv_len, positions and rows are int32 (rows: int64) device tensors;
-    max_q and max_kv bound the sequences' new tokens and cached lengths.  The
-    block that made the plan knows how many tokens each sequence holds; forward,
-    advance and replayed keep that in step."""
+    cu_q, kv_len, positions and rows are int32 (rows: int64) device tensors,
+    counts holds positions and kv_len, last the last cache row of each token's
+    sequence; max_q and max_kv bound the sequences' new tokens and cached
+    lengths.  The block that made the plan knows how many tokens each sequence
+    holds; forward, advance and replayed keep that in step."""
 
-    def __init__(self, block, number, new, cu_q, kv_len, positions, rows, max_q, max_kv, longest):
+    def __init__(self, block, number, new, cu_q, counts, rows, last, max_q, max_kv, longest):
         self.block, self.number, self.new = block, number, list(new)
-        self.cu_q, self.kv_len, self.positions, self.rows = cu_q, kv_len, positions, rows
+        self.cu_q, self.counts, self.rows, self.last = cu_q, counts, rows, last
+        self.positions, self.kv_len = counts[:rows.numel()], counts[rows.numel():]
         self.max_q, self.max_kv = max_q, max_kv
         self.steps = 0  # how often it was advanced
         self.longest = longest  # of its sequences, with the plan's tokens
 
     def advance(self):
         """The same call one token later (plans of at most one token per
-        sequence): three additions on the current stream.  The step before counts
+        sequence): three small kernels on the current stream.  The step before counts
         as run; the one that is announced counts for later plans once it has
         run, by forward, or by the next advance after a graph's replay.  The last
         step is the one whose longest sequence holds max_kv tokens."""
@@ -47,13 +49,15 @@ class Plan:
         self._shift()
 
     def _shift(self):
-        """The device's part of advance."""
-        self.positions.add_(1)
-        self.kv_len.add_(1)
+        """The device's part of advance.  Replays that pass the cache's end, which no
+        check on the host sees, write the last row of their own sequence."""
+        self.counts.add_(1)
         self.rows.add_(1)
+        torch.minimum(self.rows, self.last, out=self.rows)
 
     def replayed(self, steps: int):
-        """Note `steps` replays of a HIP graph that holds forward and then advance()."""
+        """Note `steps` replays of a HIP graph that holds forward and then advance();
+        called before them, it refuses those that would pass max_kv."""
         if any(n > 1 for n in self.new):
             raise ValueError("a plan of more than one token per sequence cannot be advanced")
         if steps < 0:
@@ -61,6 +65,8 @@ class Plan:
         self._check_place()
         if steps == 0:
             return
+        if self.longest + steps - 1 > self.max_kv:
+            raise ValueError(f"the plan's sequences would hold {self.longest + steps - 1} tokens, its bound is {self.max_kv}")
         for b in self._sequences():
             self.block.lens[b] += steps
             self.block._announced[b] = self.block.lens[b]
@@ -146,19 +152,21 @@ class AttentionBlock:
             max_kv = longest
         if not longest <= max_kv <= self.max_len:
             raise ValueError(f"max_kv must be {longest} to {self.max_len}, got {max_kv}")
-        cu, pos, rows = [0], [], []
+        cu, pos, rows, last = [0], [], [], []
         for b, n in enumerate(new):
             cu.append(cu[-1] + n)
             pos.extend(range(held[b], ends[b]))
             rows.extend(range(b * self.max_len + held[b], b * self.max_len + ends[b]))
+            last.extend([(b + 1) * self.max_len - 1] * n)
         self._plans += 1
         for b, n in enumerate(new):
             if n:  # an announced step of a sequence without new tokens keeps its place
                 self.lens[b], self._announced[b], self._owner[b] = ends[b], None, self._plans
         dev = self.cache.device
         i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
-        return Plan(self, self._plans, new, i32(cu), i32(ends), i32(pos), torch.tensor(rows, dtype=torch.int64, device=dev),
-                    max(new, default=0), max_kv, longest)
+        i64 = lambda v: torch.tensor(v, dtype=torch.int64, device=dev)  # noqa: E731
+        return Plan(self, self._plans, new, i32(cu), i32(pos + ends), i64(rows), i64(last), max(new, default=0), max_kv,
+                    longest)
 
     def workspace(self, plan: Plan):
         """The attention workspace of a plan, for callers that keep it."""

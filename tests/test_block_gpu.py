@@ -200,3 +200,39 @@ def test_chunks_after_the_step_loop(graph):
         assert np.isfinite(kv[40 * s:40 * s + n]).all() and np.isnan(kv[40 * s + n:40 * s + 40]).all()
     seqs = [(0, 2, 0, 11), (2, 4, 40, 4), (6, 1, 80, 14)]
     _check_attention(b.o[:7], None, _np(b.qkv[:7, :8]), np.nan_to_num(kv[:, :2]), np.nan_to_num(kv[:, 2:]), seqs, 64 ** -0.5, True)
+
+
+def test_replays_past_the_end_of_the_cache():
+    """A graph of forward and advance() replayed more often than there is room: the other sequences' rows keep their bits."""
+    b = _block(max_seqs=3, max_len=20, max_tokens=30)
+    print("[block] replays past the end", flush=True)
+    b.forward(_x(25, 272, 1), b.plan([4, 18, 3]))
+    step = b.plan([0, 1, 1], max_kv=20)
+    x, ws = _x(2, 272, 2), b.workspace(step)
+    start = [t.clone() for t in (step.positions, step.kv_len, step.rows)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b.forward(x, step, ws)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b.forward(x, step, ws)
+        step.advance()
+    for t, v in zip((step.positions, step.kv_len, step.rows), start):
+        t.copy_(v)
+    with pytest.raises(ValueError):
+        step.replayed(2)
+    step.replayed(1)
+    g.replay()
+    g.replay()
+    torch.cuda.synchronize()
+    held = b.cache.view(torch.int16).clone()
+    assert step.kv_len.tolist() == [6, 21, 6] and step.rows.tolist() == [39, 45]
+    for _ in range(30):
+        g.replay()
+    torch.cuda.synchronize()
+    now = b.cache.view(torch.int16)
+    assert step.rows.tolist() == [39, 59]
+    for lo, hi in ((0, 39), (40, 45)):
+        assert torch.equal(now[lo:hi], held[lo:hi])

@@ -214,3 +214,28 @@ def test_a_long_idle_sequence_does_not_bound_the_others(model, lens):
     plan = model.b.plan([0, 2])
     assert plan.max_kv == lens[1] + 5
     model.run([0, 2], plan)
+
+
+def test_replays_past_the_bound(model):
+    """replayed refuses, before the replays, those that would pass max_kv, and changes nothing; replays that were never
+    noted stay inside their sequence's rows."""
+    model.run([4, 18, 3])
+    step = model.b.plan([0, 1, 1], max_kv=20)
+    before = list(model.b.lens), step.longest
+    for n in (3, -1):
+        with pytest.raises(ValueError):
+            step.replayed(n)
+    assert (list(model.b.lens), step.longest) == before
+    step.replayed(2)
+    for _ in range(2):
+        model.replay(step)
+    for f in (step.advance, lambda: step.replayed(1)):
+        with pytest.raises(ValueError):
+            f()
+    cache = model.b.cache.clone()
+    for _ in range(30):  # 28 past the end of sequence 1, 13 past that of sequence 2, the last of the cache
+        model.b._enqueue(torch.full((2, HIDDEN), 99.0).bfloat16(), step, None)
+        step._shift()
+    # sequence 0, and all that sequences 1 and 2 hold but the last row of each
+    assert torch.equal(model.b.cache[:20].nan_to_num(), cache[:20].nan_to_num())
+    assert torch.equal(model.b.cache[20:39], cache[20:39]) and torch.equal(model.b.cache[40:45], cache[40:45])
