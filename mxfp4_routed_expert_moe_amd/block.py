@@ -180,6 +180,8 @@ class AttentionBlock:
         T = plan.rows.numel()
         if tuple(x.shape) != (T, self.hidden):
             raise ValueError(f"x must have shape {(T, self.hidden)}, got {tuple(x.shape)}")
+        if T == 0:
+            return self.y[:0]
         if plan.longest > plan.max_kv:
             raise ValueError(f"the plan was advanced to {plan.longest} tokens, its bound is {plan.max_kv}")
         if plan.steps:

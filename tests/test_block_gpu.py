@@ -236,3 +236,12 @@ def test_replays_past_the_end_of_the_cache():
     assert step.rows.tolist() == [39, 59]
     for lo, hi in ((0, 39), (40, 45)):
         assert torch.equal(now[lo:hi], held[lo:hi])
+
+
+def test_a_plan_of_no_tokens():
+    b = _block()
+    print("[block] no tokens", flush=True)
+    for new in ([], [0, 0]):
+        plan = b.plan(new)
+        assert b.forward(_x(0, 272, 1), plan, b.workspace(plan)).shape == (0, 272)
+    assert b.lens == [0, 0, 0, 0]

@@ -239,3 +239,16 @@ def test_replays_past_the_bound(model):
     # sequence 0, and all that sequences 1 and 2 hold but the last row of each
     assert torch.equal(model.b.cache[:20].nan_to_num(), cache[:20].nan_to_num())
     assert torch.equal(model.b.cache[20:39], cache[20:39]) and torch.equal(model.b.cache[40:45], cache[40:45])
+
+
+@pytest.mark.parametrize("new", [[], [0], [0, 0, 0]])
+def test_a_plan_of_no_tokens(model, new):
+    model.run([3, 1])
+    plan = model.b.plan(new)
+    calls = len(model.calls)
+    assert model.b.forward(torch.empty(0, HIDDEN).bfloat16(), plan).shape == (0, HIDDEN)
+    plan.advance()
+    assert len(model.calls) == calls
+    with pytest.raises(ValueError):
+        model.b.forward(torch.empty(1, HIDDEN).bfloat16(), plan)
+    model.run([1, 1, 1])
