@@ -46,6 +46,7 @@ typedef __attribute__((__vector_size__(8 * sizeof(short)))) short s16x8;
 
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLazy = 8.0f;  // log2 of how far a row's maximum may rise before the output is rescaled
+constexpr float kLargeScore = 0x1p16f;  // base-two score from which the maximum is subtracted before the scale
 
 __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -162,7 +163,17 @@ __device__ __forceinline__ void attend(const uint8_t* ks, const uint8_t* vs, con
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) st.o[i] *= alpha;
   }
-  const float mc = st.m == kNegInf ? 0.f : st.m * c;
+  // A weight's exponent is one FMA, s c - m c, whose m c is rounded: off by 2^-24 of
+  // it, no more than the rounding of s itself costs, and the same for all the weights
+  // of the tile.  But where m c is large that is too much for an exponent (from
+  // 2^31 on the weights would all be 0 or infinite), so there m is subtracted first.
+  float mc = st.m == kNegInf ? 0.f : st.m * c;
+  if (__any(fabsf(mc) > kLargeScore)) {
+    const float m = st.m == kNegInf ? 0.f : st.m;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) s[t] -= m;
+    mc = 0.f;
+  }
   // The weights are summed as rounded, so that their rounding leaves a row's
   // weights normalised: one dot product with ones per pair.
   const bf16x2 ones = {static_cast<__bf16>(1.f), static_cast<__bf16>(1.f)};

@@ -647,3 +647,34 @@ def test_attention_prompts_past_max_q_without_max_kv(lq, max_q, Hq, Hkv, D, caus
     _check_attention(out, lse, q, k, v, rows, D ** -0.5, False)
     for a, n, _, _ in seqs:
         assert torch.all(out[a + max_q:a + n] == 9) and torch.all(lse[a + max_q:a + n] == 3)
+
+
+@pytest.mark.parametrize("lq,lk,Hq,Hkv,D", [(3, 40, 2, 2, 64), (3, 9000, 4, 1, 128), (70, 300, 2, 1, 128), (70, 9000, 2, 1, 64),
+                                            (3, 3000, 4, 2, 256)])
+@pytest.mark.parametrize("power", [-30, -10, 0, 40, 60, 85, 87.4, 100])
+def test_attention_large_scores(lq, lk, Hq, Hkv, D, power):
+    """Scores of +-2^(40 + power) and up to twice that, past float32's range at the end.  Every score is exact and two
+    that differ do so by 2^(33 + power) or more: one key, or the mean of those that tie, takes all the weight (at 2^3
+    between neighbours, -30, the others have at most 3000 e^-8 of it)."""
+    _say("attention large scores", lq, lk, Hq, Hkv, D, power)
+    g = np.random.default_rng(17)
+    q = np.zeros((lq, Hq, D))
+    q[0, :, 0], q[1, :, 0] = -2.0 ** 20, 2.0 ** 20  # the others: every score zero
+    k, v = R.bf16(g.normal(0, 1, (lk, Hkv, D))), R.bf16(g.normal(0, 1, (lk, Hkv, D)))
+    k[:, :, 0] = R.bf16(2.0 ** 20 * g.uniform(1, 2, (lk, Hkv)))
+    scale = float(np.float32(2.0 ** power))
+    out, lse = _run(_bf16(q), _bf16(k), _bf16(v), [0, lq], [(0, lq, 0, lk)], True, scale=scale)
+    y, l = _np(out), _np(lse)
+    for i, h in ((i, h) for i in (0, 1) for h in range(Hq)):
+        kk, vv = k[:lk - lq + 1 + i, h // (Hq // Hkv), 0], v[:lk - lq + 1 + i, h // (Hq // Hkv)]
+        z = q[i, h, 0] * kk
+        p = np.exp(np.maximum((z - z.max()) * scale, -700))
+        want, A = p @ vv / p.sum(), p @ np.abs(vv) / p.sum()
+        # roundings of the result and of the weights; an exponent below 2^16 is off by 2^-8 or less, larger ones differ exactly
+        assert np.all(np.abs(y[i, h] - want) <= U * np.abs(want) + (2 * U + 2 * np.expm1(2.0 ** -8) + (lk + 64) * 2.0 ** -23) * A)
+        ref = z.max() * scale + np.log(p.sum())
+        with np.errstate(over="ignore"):
+            far = np.isinf(np.float32(ref))
+        assert l[i, h] == np.sign(ref) * np.inf if far else abs(l[i, h] - ref) <= 2.0 ** -20 * abs(ref) + 2 * U
+    rest = list(range(2, lq))
+    _check_attention(out[rest], lse[rest], q[rest], k, v, [(j, 1, 0, lk - lq + 1 + i) for j, i in enumerate(rest)], scale, False)
