@@ -342,9 +342,11 @@ __device__ __forceinline__ void load_q(const AttnArgs& a, const LaneRow& x, bf16
 }
 
 // Outputs d .. d + 3 of a row from the sums o and l over the maximum m.  l is 0
-// only where the row saw no key: its largest weight is at least 2^-kLazy.
+// only where the row saw no score above -infinity: its largest weight is at least
+// 2^-kLazy.  Such a row gives zeros; o may hold infinite values times 0.
 __device__ __forceinline__ void store_quad(const AttnArgs& a, int64_t q_row, int head, int d, f32x4 o, float m,
                                            float l) {
+  if (l == 0.f) o = f32x4{0.f, 0.f, 0.f, 0.f};
   const float inv = l == 0.f ? 0.f : 1.f / l;
   u32x2 v;
 #pragma unroll

@@ -678,3 +678,22 @@ def test_attention_large_scores(lq, lk, Hq, Hkv, D, power):
         assert l[i, h] == np.sign(ref) * np.inf if far else abs(l[i, h] - ref) <= 2.0 ** -20 * abs(ref) + 2 * U
     rest = list(range(2, lq))
     _check_attention(out[rest], lse[rest], q[rest], k, v, [(j, 1, 0, lk - lq + 1 + i) for j, i in enumerate(rest)], scale, False)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("lq,lk,Hq,Hkv,D", [(2, 3, 2, 2, 64), (2, 70, 4, 1, 128), (70, 200, 2, 1, 64), (2, 3000, 4, 2, 256),
+                                            (70, 9000, 2, 1, 128)])
+def test_attention_rows_whose_every_score_is_minus_infinity(lq, lk, Hq, Hkv, D, bad):
+    """They give zeros and lse -infinity, whatever the values that they see."""
+    _say("attention all scores -inf", lq, lk, Hq, Hkv, D, bad)
+    g = np.random.default_rng(18)
+    q = R.bf16(g.normal(0, 1, (lq, Hq, D)))
+    k, v = R.bf16(g.normal(0, 1, (lk, Hkv, D))), R.bf16(g.normal(0, 1, (lk, Hkv, D)))
+    k[:, :, 0] = np.inf                    # times -1: -infinity
+    q[0], q[0, :, 0], q[1:, :, 0] = 0, -1, -1
+    q[0, :, 1:] = 0
+    k[:, :, 1:] = R.bf16(g.normal(0, 1, (lk, Hkv, D - 1)))
+    v[::3, :, 5] = bad
+    v[lk - 1, :, 7] = bad
+    out, lse = _run(_bf16(q), _bf16(k), _bf16(v), [0, lq], [(0, lq, 0, lk)], True)
+    assert torch.all(out == 0) and torch.all(lse == -float("inf"))
