@@ -160,6 +160,13 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(NormArgs a) {
     if (INTER) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
+      // An infinite norm: an element that is not rotated must not meet a neighbour's
+      // infinity, not even times its B of 0.  (Chosen always, 2049 x 65 heads 18.6 us
+      // against 14.1.)
+      if (__any(f == 0.f)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = rot ? y[j] : x[j];
+      }
     } else {
       u32x4 other;
 #pragma unroll

@@ -697,3 +697,23 @@ def test_attention_rows_whose_every_score_is_minus_infinity(lq, lk, Hq, Hkv, D, 
     v[lk - 1, :, 7] = bad
     out, lse = _run(_bf16(q), _bf16(k), _bf16(v), [0, lq], [(0, lq, 0, lk)], True)
     assert torch.all(out == 0) and torch.all(lse == -float("inf"))
+
+
+@pytest.mark.parametrize("T,Hq,Hk", [(2, 3, 1), (900, 40, 8)])
+@pytest.mark.parametrize("off,Rd", [(0, 32), (32, 32), (8, 16)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_qk_norm_rope_an_infinity_beside_the_rotated_part(T, Hq, Hk, off, Rd, interleaved):
+    """A head with one infinity gives zeros (their share of an infinite norm) and NaN where the infinity enters: itself, and
+    its rotated partner; an element that is not rotated has no partner."""
+    _say("qk_norm_rope infinity", T, Hq, Hk, off, Rd, interleaved)
+    g = np.random.default_rng(off + Rd)
+    D = 64
+    q, k = R.bf16(g.normal(0, 1, (T, Hq, D))), R.bf16(g.normal(0, 1, (T, Hk, D)))
+    n = min(D, T * Hq)                     # one element each of up to 64 heads, all of them different
+    q.reshape(-1, D)[np.arange(n) * (T * Hq // n), (11 * np.arange(n) + 3) % D] = np.inf
+    k[0, 0, D - 2] = -np.inf
+    qw, pos = np.float32(g.normal(1, 0.2, D)), g.integers(0, 30, T).astype(np.int32)
+    cs = _table(30, Rd)
+    qo, ko = A.qk_norm_rope(_bf16(q), _bf16(k), _gpu(qw), None, _gpu(pos), _gpu(cs), rot_offset=off, interleaved=interleaved)
+    _check_rope(qo, q, qw, pos, cs, off, interleaved, 1e-6)
+    _check_rope(ko, k, None, pos, cs, off, interleaved, 1e-6)
