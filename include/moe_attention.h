@@ -99,7 +99,8 @@ typedef struct moe_heads {
  * Requirements: head_dim a multiple of 8 up to 512; rot_dim a multiple of 16
  * (0 = no rotation), rot_offset a multiple of 8, rot_offset + rot_dim <=
  * head_dim; 1 <= q_heads, 0 <= k_heads, q_heads + k_heads <= 1024, T * (q_heads +
- * k_heads) < 2^28 (MOE_ESHAPE otherwise); eps >= 0 (MOE_EINVAL).
+ * k_heads) < 2^28, for a head_dim above 256 with the heads rounded up to a multiple of
+ * four (MOE_ESHAPE otherwise); eps >= 0 (MOE_EINVAL).
  */
 int moe_qk_norm_rope(const moe_heads* q, int32_t q_heads, const moe_heads* k, int32_t k_heads, int32_t T,
                      int32_t head_dim, const float* q_weight, const float* k_weight, float eps,

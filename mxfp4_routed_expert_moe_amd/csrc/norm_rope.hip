@@ -242,6 +242,8 @@ extern "C" int moe_qk_norm_rope(const moe_heads* q, int32_t q_heads, const moe_h
   if (T > MOE_MAX_TOKENS || q_heads < 1 || q_heads > 1024 || k_heads > 1024 - q_heads) return MOE_ESHAPE;
   if (static_cast<int64_t>(T) * (q_heads + k_heads) >= (1 << 28)) return MOE_ESHAPE;  // 2^32 threads
   if (head_dim < 8 || head_dim > 512 || head_dim % 8 != 0) return MOE_ESHAPE;
+  // heads wider than 256 take 64 lanes per four heads: again 2^32 threads
+  if (head_dim > 256 && static_cast<int64_t>(T) * ((q_heads + k_heads + 3) / 4 * 4) >= (1 << 28)) return MOE_ESHAPE;
   if (rot_dim % 16 != 0 || rot_offset % 8 != 0 || rot_dim > head_dim || rot_offset > head_dim - rot_dim)
     return MOE_ESHAPE;
   if (!(eps >= 0.f) || (interleaved != 0 && interleaved != 1)) return MOE_EINVAL;

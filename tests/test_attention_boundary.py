@@ -231,3 +231,10 @@ def test_fp8_linear_workspace_grows_with_every_size():
 
 def test_attention_scale_whose_base_two_form_overflows():
     assert _attn(scale=2.0 ** 127 * 1.5) == EINVAL
+
+
+def test_qk_norm_rope_grid_of_wide_heads():
+    """A group of 64 lanes takes four heads wider than 256: 2^18 tokens of 1021 to 1023 heads are 2^32 threads."""
+    for D in (264, 512):
+        for Hk in (21, 22, 23):
+            assert _rope(T=B.MOE_MAX_TOKENS, Hq=1000, Hk=Hk, D=D) == ESHAPE
