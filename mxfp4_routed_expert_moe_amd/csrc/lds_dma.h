@@ -7,12 +7,6 @@
 
 namespace moe {
 
-__device__ __forceinline__ void dma16(const void* src, void* lds) {
-  __builtin_amdgcn_global_load_lds(src, lds, 16, 0, 0);
-}
-__device__ __forceinline__ void dma4(const void* src, void* lds) {
-  __builtin_amdgcn_global_load_lds(src, lds, 4, 0, 0);
-}
 // 16 bytes per lane from byte `offset` + `uniform` of a buffer resource.
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, int offset, int uniform, void* lds) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, lds, 16, offset, uniform, 0, 0);
