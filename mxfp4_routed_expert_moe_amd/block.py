@@ -37,6 +37,7 @@ class Plan:
         self.positions, self.kv_len = counts[:rows.numel()], counts[rows.numel():]
         self.max_q, self.max_kv = max_q, max_kv
         self.steps = 0  # how often it was advanced
+        self.cancelled = False
         self.longest = longest  # of its sequences, with the plan's tokens
 
     def advance(self):
@@ -62,7 +63,7 @@ class Plan:
             raise ValueError("a plan of more than one token per sequence cannot be advanced")
         if steps < 0:
             raise ValueError(f"steps must not be negative, got {steps}")
-        self._check_place()
+        self._check(advance=True)
         if steps == 0:
             return
         if self.longest + steps - 1 > self.max_kv:
@@ -70,18 +71,41 @@ class Plan:
         for b in self._sequences():
             self.block.lens[b] += steps
             self.block._announced[b] = self.block.lens[b]
+        self._ran()
         self.steps += steps
         self.longest += steps
+
+    def cancel(self):
+        """Give the plan's tokens back: it will not run.  Only before it has run, and before
+        the plans that were made after it for its sequences are cancelled or reset."""
+        at = [b for b in self._sequences() if self.number > self.block._since[b]]
+        if self.cancelled or any(self.block._unrun[b][-1:] != [self.number] for b in at):
+            raise ValueError("the plan has run, was cancelled, or is not the last one of its sequences")
+        self.cancelled = True
+        for b in at:
+            self.block.lens[b] -= self.new[b]
+            self.block._unrun[b].pop()
+            self.block._owner[b] = 0
 
     def _sequences(self):
         """The sequences that the plan brings tokens to."""
         return [b for b, n in enumerate(self.new) if n]
 
-    def _check_place(self):
-        """The next token of a sequence is this plan's to bring until a later plan brings one."""
+    def _check(self, advance=False):
+        """Whether the plan's step can run now: the plans before it have, and, once it is
+        advanced, no later plan has brought the token that would be its next."""
         for b in self._sequences():
-            if self.block._owner[b] != self.number:
+            if self.cancelled or self.number <= self.block._since[b]:
+                raise ValueError(f"the plan was cancelled, or sequence {b} reset: make a new plan")
+            if self.block._unrun[b] and self.block._unrun[b][0] < self.number:
+                raise ValueError(f"a plan made before this one for sequence {b} has not run: run it, or cancel it")
+            if (self.steps or advance) and self.block._owner[b] != self.number:
                 raise ValueError(f"a later plan has brought tokens to sequence {b}: make a new plan")
+
+    def _ran(self):
+        for b in self._sequences():
+            if self.number in self.block._unrun[b]:
+                self.block._unrun[b].remove(self.number)
 
 
 class AttentionBlock:
@@ -112,6 +136,8 @@ class AttentionBlock:
         self.lens = [0] * max_seqs  # tokens that each sequence holds once its plans and their announced steps have run
         self._announced = [None] * max_seqs  # what lens is with a step that was announced and has not run
         self._owner = [0] * max_seqs  # the number of the last plan that brought tokens
+        self._unrun = [[] for _ in range(max_seqs)]  # the numbers of the plans that have not run
+        self._since = [0] * max_seqs  # plans up to this number ended with a reset
         self._plans = 0
         self.cache = torch.empty((max_seqs * max_len, 2 * kv_heads, head_dim), dtype=bf16, device=dev)
         self.kv_start = torch.arange(0, max_seqs * max_len, max_len, dtype=torch.int32, device=dev)
@@ -127,17 +153,19 @@ class AttentionBlock:
         return self.lens[b] - (self._announced[b] == self.lens[b])
 
     def reset(self, b=None):
-        """Forget the tokens of sequence b (None: of all): its next plan begins at position 0."""
+        """Forget the tokens of sequence b (None: of all) and the plans that bring it some: its next
+        plan begins at position 0."""
         if b is not None and not 0 <= b < self.max_seqs:
             raise ValueError(f"there are {self.max_seqs} sequences, got {b}")
-        self._plans += 1  # no earlier plan can be advanced there
+        self._plans += 1
         for s in range(self.max_seqs) if b is None else (b,):
-            self.lens[s], self._announced[s], self._owner[s] = 0, None, self._plans
+            self.lens[s], self._announced[s], self._owner[s] = 0, None, 0
+            self._unrun[s], self._since[s] = [], self._plans
 
     def plan(self, new, max_kv=None) -> Plan:
         """A call that brings new[b] tokens to sequence b, after those it holds (host
         list; fewer entries than max_seqs: the first ones).  Plans run in the order in
-        which they were made.  max_kv: the bound on the cached lengths of the sequences
+        which they were made; one that is not to run is cancelled.  max_kv: the bound on the cached lengths of the sequences
         that get tokens, this call's by default; a plan that is to be advanced passes the one of its last step."""
         if len(new) > self.max_seqs or any(n < 0 for n in new):
             raise ValueError(f"new must hold up to {self.max_seqs} counts")
@@ -158,15 +186,17 @@ class AttentionBlock:
             pos.extend(range(held[b], ends[b]))
             rows.extend(range(b * self.max_len + held[b], b * self.max_len + ends[b]))
             last.extend([(b + 1) * self.max_len - 1] * n)
+        dev = self.cache.device
+        i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+        i64 = lambda v: torch.tensor(v, dtype=torch.int64, device=dev)  # noqa: E731
+        plan = Plan(self, self._plans + 1, new, i32(cu), i32(pos + ends), i64(rows), i64(last), max(new, default=0), max_kv,
+                    longest)
         self._plans += 1
         for b, n in enumerate(new):
             if n:  # an announced step of a sequence without new tokens keeps its place
                 self.lens[b], self._announced[b], self._owner[b] = ends[b], None, self._plans
-        dev = self.cache.device
-        i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
-        i64 = lambda v: torch.tensor(v, dtype=torch.int64, device=dev)  # noqa: E731
-        return Plan(self, self._plans, new, i32(cu), i32(pos + ends), i64(rows), i64(last), max(new, default=0), max_kv,
-                    longest)
+                self._unrun[b].append(self._plans)
+        return plan
 
     def workspace(self, plan: Plan):
         """The attention workspace of a plan, for callers that keep it."""
@@ -184,9 +214,9 @@ class AttentionBlock:
             return self.y[:0]
         if plan.longest > plan.max_kv:
             raise ValueError(f"the plan was advanced to {plan.longest} tokens, its bound is {plan.max_kv}")
-        if plan.steps:
-            plan._check_place()
+        plan._check()
         y = self._enqueue(x, plan, ws)
+        plan._ran()
         for b in plan._sequences():
             if self._owner[b] == plan.number:
                 self._announced[b] = None

@@ -252,3 +252,38 @@ def test_a_plan_of_no_tokens(model, new):
     with pytest.raises(ValueError):
         model.b.forward(torch.empty(1, HIDDEN).bfloat16(), plan)
     model.run([1, 1, 1])
+
+
+def test_a_plan_that_never_ran(model):
+    """Its tokens lie before those of later plans: these are refused until it has run, or gave its tokens back."""
+    model.run([3, 4, 1])
+    lost = model.b.plan([2, 0, 1])
+    other = model.b.plan([0, 2])
+    after = model.b.plan([1, 1], max_kv=20)
+    with pytest.raises(ValueError):
+        model.b.forward(torch.zeros(2, HIDDEN).bfloat16(), after)
+    with pytest.raises(ValueError):
+        after.replayed(1)
+    with pytest.raises(ValueError):  # a later plan goes on from its tokens
+        lost.cancel()
+    model.run([0, 2], other)
+    after.cancel()
+    lost.cancel()
+    assert model.b.lens == [3, 6, 1]
+    for f in (lambda: model.b.forward(torch.zeros(3, HIDDEN).bfloat16(), lost), lost.cancel, after.advance, other.cancel):
+        with pytest.raises(ValueError):
+            f()
+    model.run([2, 1, 1])
+
+
+def test_reset_forgets_plans_that_never_ran(model):
+    lost = model.b.plan([2, 3])
+    model.b.reset(0)
+    model.run([4])
+    with pytest.raises(ValueError):
+        model.b.forward(torch.zeros(5, HIDDEN).bfloat16(), lost)
+    with pytest.raises(ValueError):
+        model.run([1, 1])
+    model.b.reset()
+    model.fed = [[], [], []]
+    model.run([1, 1])
