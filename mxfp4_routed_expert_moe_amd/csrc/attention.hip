@@ -740,8 +740,8 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //     263; head_dim 256, 32 x up to 4096: 123; 8 units 129, 32 units 141), until
 //     kRounds blocks a CU, which are even enough, and bound the workspace.
 // Many rows: blocks wanted as above (head_dim 128: 288 tiles, 4 x 256 queries after
-//     4096 keys 51, with one 67; 256: 264 tiles, 512 queries after 16384 keys 174,
-//     with two 191); pieces of at least tiles / 16 key tiles, 4 to 16, as a join
+//     4096 keys 51, with one 67; 256: 66 tiles, 512 queries over 16384 keys, 16 heads
+//     over 2, in 4 pieces 168 to 197, with two 191); pieces of at least tiles / 16 key tiles, 4 to 16, as a join
 //     costs more the more rows there are (32 row tiles, 2 x 64 queries, 2048 keys, 4:
 //     13.2, 8: 15.8, 16: 21.4; 144, a prompt of 1024, 4: 17.8, 8: 16.9, 16: 17.9;
 //     264, a prompt of 1024, 8: 35.4, 16: 28.2).
