@@ -741,8 +741,9 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //     kRounds blocks a CU, which are even enough, and bound the workspace.
 // Many rows: blocks wanted as above (head_dim 128: 288 tiles, 4 x 256 queries after
 //     4096 keys 51, with one 67; 256: 66 tiles, 512 queries over 16384 keys, 16 heads
-//     over 2, in 4 pieces 168 to 197, with two 191); pieces of at least tiles / 16 key tiles, 4 to 16, as a join
-//     costs more the more rows there are (32 row tiles, 2 x 64 queries, 2048 keys, 4:
+//     over 2, in 4 pieces 174, with two 191, in turn; 168 to 197 between sessions);
+//     pieces of at least tiles / 16 key tiles, 4 to 16, as a join costs more the more
+//     rows there are (32 row tiles, 2 x 64 queries, 2048 keys, 4:
 //     13.2, 8: 15.8, 16: 21.4; 144, a prompt of 1024, 4: 17.8, 8: 16.9, 16: 17.9;
 //     264, a prompt of 1024, 8: 35.4, 16: 28.2).
 constexpr int kRounds = 64;

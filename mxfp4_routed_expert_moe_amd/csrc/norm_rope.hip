@@ -13,9 +13,9 @@
 //
 // Bound by HBM: 16384 tokens of 40 heads of 128 are 344 MB in 79 us = 4.4 TB/s (a large
 // copy moves 5.2 TB/s).  Four heads per group 79 us, two 83, eight 87; the stores past
-// the caches 79 against 85, by the operator alone: what reads q and k right after
-// it, as attention does, then takes them from memory.  A call of a few tokens is one
-// launch, 2.5 us.
+// the caches 79 against 85, timed by the operator alone (with attention behind it,
+// which reads q and k again, not compared).  A call of a few tokens is one launch,
+// 2.5 us.
 #include <math.h>
 
 #include "../../include/moe_attention.h"
