@@ -1,0 +1,969 @@
+// Softmax attention over a paged cache (include/moe_paged.h, moe_paged_attention).
+//
+// Rows, tiles and their arithmetic are those of the attention over a contiguous cache
+// (attention_core.h): the query heads of a key head are folded into rows, row r
+// is query r / G, head r % G.  What differs is where keys come from.  A DMA instruction
+// fills at most 16 rows of a tile, and a page holds a multiple of 16 keys, so every
+// instruction has one page and the tile's keys need one lookup per 16 ("half" below: 16 keys).
+//
+// Three kernels write shares of rows, a fourth joins them:
+//  token  32 rows of a sequence (its new tokens' heads, few of them), the waves split
+//         the keys; the sequence's own keys, or those of listed blocks
+//  rows   128 rows of a sequence over its own keys, or of a whole group over
+//         the prefix that its sequences share
+// With a shared prefix a row has shares of both: slots 0 .. prefix_splits - 1 are the
+// prefix's, the others the sequence's own.  Every slot of a row is written, if only
+// with a sum of 0, so the join needs to know nothing about groups or lists.
+#include <math.h>
+
+#include <algorithm>
+
+#include "attention_core.h"
+#include "paged_internal.h"
+
+namespace moe {
+
+namespace {
+
+struct PagedArgs {
+  PagedSeqs s;
+  moe_heads q, out;
+  moe_pages k, v;
+  const int32_t *cu_group, *prefix_len, *blocks;
+  float* lse;
+  float* part_o;    // [slots, q_rows, q_heads, D]
+  float2* part_ml;  // [slots, q_rows, q_heads]: maximum, sum
+  int q_heads, kv_heads, group, max_q, max_kv, n_groups, max_prefix, n_blocks;
+  int chunk;         // own keys (listed blocks) of a split
+  int prefix_chunk;  // prefix keys of a split
+  int prefix_splits, slots;
+  int one_tile;      // every sequence is one tile of the token kernel
+  int token;         // the token kernel did the own keys
+  int tile_rows;     // rows of a tile of the kernel that did the own keys
+  int join_rows;     // rows of a block of the join
+  float scale, c;    // c = scale * log2(e)
+  __host__ __device__ bool every_slot() const { return n_groups > 0 || n_blocks > 0; }
+};
+
+// ---------------------------------------------------------------- work
+// The prefix length that sequence b's group names (0 without one).  The last group
+// that begins at or before b.
+__device__ __forceinline__ int prefix_of(const PagedArgs& a, int b) {
+  if (a.n_groups == 0) return 0;
+  int lo = 0, hi = a.n_groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (a.cu_group[mid] <= b) lo = mid; else hi = mid;
+  }
+  const GroupRange g = group_range(a.cu_group, lo, a.s.n_seqs);
+  return b >= g.first && b < g.past ? a.prefix_len[lo] : 0;
+}
+
+__device__ __forceinline__ PagedRange sequence(const PagedArgs& a, int b, int prefix) {
+  return paged_range(a.s.cu_q, a.s.kv_len, b, a.s.q_rows, a.s.capacity, prefix, a.max_prefix, a.max_kv, a.s.shift);
+}
+
+struct PagedTile : PagedRange {
+  int seq;  // whose row of the table names the pages
+  int tile, tiles;
+};
+
+// Tile t over all sequences (each sequence's tiles in a row), 64 of them at a time.
+__device__ bool find_tile(const PagedArgs& a, int t, int rows, PagedTile& w) {
+  const int lane = threadIdx.x & 63;
+  for (int base = 0; base < a.s.n_seqs; base += 64) {
+    int nt = 0;
+    if (base + lane < a.s.n_seqs)
+      nt = (min(sequence(a, base + lane, 0).lq, a.max_q) * a.group + rows - 1) / rows;
+    const int incl = wave_incl_scan(nt);
+    const uint64_t past = __ballot(incl > t);
+    if (past) {
+      const int src = __ffsll(static_cast<unsigned long long>(past)) - 1;
+      w.seq = uniform(base + src);
+      w.tiles = uniform(__shfl(nt, src, 64));
+      w.tile = uniform(t - (__shfl(incl, src, 64) - w.tiles));
+      return true;
+    }
+    t -= uniform(__shfl(incl, 63, 64));
+  }
+  return false;
+}
+
+__device__ __forceinline__ void load_range(const PagedArgs& a, PagedTile& w) {
+  const PagedRange r = sequence(a, w.seq, prefix_of(a, w.seq));
+  w.q0 = uniform(r.q0), w.lq = uniform(r.lq), w.diag = uniform(r.diag);
+  w.own = uniform(r.own), w.end = uniform(r.end);
+}
+
+// Tile t over all groups: 128-row tiles of the rows of a group's sequences, in groups
+// that share something.
+__device__ bool find_group_tile(const PagedArgs& a, int t, int rows, PagedTile& w, GroupRange& g) {
+  const int lane = threadIdx.x & 63;
+  for (int base = 0; base < a.n_groups; base += 64) {
+    int nt = 0, q0 = 0, lq = 0, keys = 0;
+    GroupRange x = {0, 0};
+    if (base + lane < a.n_groups) {
+      x = group_range(a.cu_group, base + lane, a.s.n_seqs);
+      keys = shared_keys(a.prefix_len[base + lane], a.max_prefix, a.s.shift);
+      q0 = min(max(a.s.cu_q[x.first], 0), a.s.q_rows);
+      lq = min(max(a.s.cu_q[x.past], q0), a.s.q_rows) - q0;
+      nt = keys > 0 ? (lq * a.group + rows - 1) / rows : 0;
+    }
+    const int incl = wave_incl_scan(nt);
+    const uint64_t past = __ballot(incl > t);
+    if (past) {
+      const int src = __ffsll(static_cast<unsigned long long>(past)) - 1;
+      g.first = uniform(__shfl(x.first, src, 64));
+      g.past = uniform(__shfl(x.past, src, 64));
+      w.seq = g.first;
+      w.q0 = uniform(__shfl(q0, src, 64));
+      w.lq = uniform(__shfl(lq, src, 64));
+      w.own = 0;
+      w.end = uniform(__shfl(keys, src, 64));
+      w.diag = 0;
+      w.tiles = uniform(__shfl(nt, src, 64));
+      w.tile = uniform(t - (__shfl(incl, src, 64) - w.tiles));
+      return true;
+    }
+    t -= uniform(__shfl(incl, 63, 64));
+  }
+  return false;
+}
+
+// A lane's row: the query row and head it reads and writes, and the last key it sees.
+struct LaneRow {
+  int64_t q_row;
+  int head, limit;
+  bool valid;
+};
+__device__ __forceinline__ LaneRow lane_row(const PagedArgs& a, const PagedTile& w, int kv_head, int r, int n_rows) {
+  LaneRow x;
+  x.valid = r < n_rows;
+  const int rc = min(r, n_rows - 1);
+  const int pos = rc / a.group;
+  x.q_row = w.q0 + pos;
+  x.head = kv_head * a.group + rc - pos * a.group;
+  x.limit = last_key(w, pos);
+  return x;
+}
+
+template <int D>
+__device__ __forceinline__ void load_q(const PagedArgs& a, const LaneRow& x, bf16x8 (&q)[D / 16]) {
+  const uint16_t* p = a.q.base + x.q_row * a.q.row_stride + x.head * a.q.head_stride + 8 * ((threadIdx.x & 63) >> 5);
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) q[i] = __builtin_bit_cast(bf16x8, ld16(p + 16 * i));
+}
+
+// Outputs d .. d + 3 of a row from the sums o and l over the maximum m; l is 0 only
+// where the row saw no score above -infinity: zeros then, whatever o holds.
+__device__ __forceinline__ void store_quad(const PagedArgs& a, int64_t q_row, int head, int d, f32x4 o, float m,
+                                           float l) {
+  if (l == 0.f) o = f32x4{0.f, 0.f, 0.f, 0.f};
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  u32x2 v;
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    v[e] = float_to_bf16_bits(o[2 * e] * inv) | static_cast<uint32_t>(float_to_bf16_bits(o[2 * e + 1] * inv)) << 16;
+  *reinterpret_cast<u32x2*>(a.out.base + q_row * a.out.row_stride + head * a.out.head_stride + d) = v;
+  if (a.lse && d == 0) a.lse[q_row * a.q_heads + head] = l == 0.f ? kNegInf : m * a.scale + logf(l);
+}
+
+// A slot's share of a row: the unscaled output, the maximum and the sum.
+__device__ __forceinline__ int64_t part_row(const PagedArgs& a, int slot, int64_t q_row, int head) {
+  return (static_cast<int64_t>(slot) * a.s.q_rows + q_row) * a.q_heads + head;
+}
+__device__ __forceinline__ void empty_share(const PagedArgs& a, int slot, int64_t q_row, int head) {
+  a.part_ml[part_row(a, slot, q_row, head)] = make_float2(kNegInf, 0.f);
+}
+
+// A tile whose rows see some of its 16-key halves only, or none: as attend_masked of the
+// contiguous kernels, with a limit per half; row(i): the values of half i's first key.
+template <int D, int NT, typename Row>
+__device__ __forceinline__ void attend_halves(const uint8_t* ks, const uint8_t* vs, const bf16x8 (&q)[D / 16],
+                                              RowState<D>& st, float c, const Limits<NT>& lim, int64_t row_stride,
+                                              Row row) {
+  const bool dirty = any_not_finite(vs, NT * 32 * 2 * D);
+  attend<D, NT, true>(ks, vs, q, st, c, lim, dirty);
+  if (!dirty) return;
+  const int h = (threadIdx.x & 63) >> 5;
+  for (int r = 0; r < NT * 32; ++r) {
+    int last = lim.at[0];
+#pragma unroll
+    for (int i = 1; i < 2 * NT; ++i) last = r >= 16 * i ? lim.at[i] : last;
+    if (r > last) continue;
+    add_not_finite<D>(row(r >> 4) + (r & 15) * row_stride + 4 * h, st);
+  }
+}
+
+// LDS-DMA: an instruction fills 1 KiB, 512 / D rows; the lane that lands in slot s of
+// row r loads the chunk whose slot that is (the XOR is its own inverse, and the same
+// for rows 16 apart).  Byte offset for instruction i of a half.
+template <int D, bool VALUE>
+__device__ __forceinline__ int half_offset(int i, int row_bytes) {
+  constexpr int kChunks = D / 8;
+  const int lane = threadIdx.x & 63;
+  const int r = i * (64 / kChunks) + lane / kChunks, s = lane % kChunks;
+  return r * row_bytes + 16 * (VALUE ? v_slot<D>(r, s) : k_slot<D>(r, s));
+}
+
+// Sixteen keys: where they are, and the position of the first.
+struct Half {
+  int page, key;     // a page that there is
+  uint32_t visible;  // of the tile's tokens: bit (token - the tile's first); 0 where the page is none
+};
+
+__device__ __forceinline__ const uint16_t* half_base(const moe_pages& p, const Half& x, int slot_mask, int kv_head) {
+  return p.base + x.page * p.page_stride + (x.key & slot_mask) * p.row_stride + kv_head * p.head_stride;
+}
+
+// The half at key `key` of the table row, for every token.
+__device__ __forceinline__ Half table_half(const PagedArgs& a, ConstInts table, int key) {
+  Half x;
+  const int p = table[min(key >> a.s.shift, a.s.table_pages - 1)];
+  const bool ok = p >= 0 && p < a.s.n_pages;
+  x.page = ok ? p : 0;
+  x.key = key;
+  x.visible = ok ? ~0u : 0u;
+  return x;
+}
+
+// ---------------------------------------------------------------- few rows
+constexpr int kRowsT = 32;  // rows of a tile
+constexpr int kKeysT = 32;  // keys of a wave's tile
+constexpr int kList = 512;  // listed blocks of a split
+constexpr int kWords = 1024;  // 32-block words of the marks: blocks per sequence / 32
+template <int D>
+constexpr int token_waves() { return D == 256 ? 2 : 4; }
+
+// The listed blocks of a tile's tokens, each once and ascending: entries lo .. lo +
+// count - 1 of that list.  An entry is a page, its block and the tokens that list it.
+struct ListEntry {
+  int page, block;
+  uint32_t tokens;
+};
+
+// Marks are set with integer atomics (their order changes nothing) in LDS, one bit a
+// block; a block's place in the list is the number of marks below it.  scratch: at
+// least 2 * kWords + 16 ints.  Returns the entries from lo on, at most `count`.
+template <int THREADS>
+__device__ int build_list(const PagedArgs& a, const PagedTile& w, int kv_head, int tok0, int n_tok, int lo, int count,
+                          ListEntry* list, uint32_t* scratch) {
+  const int tid = threadIdx.x;
+  uint32_t* marks = scratch;
+  int* below = reinterpret_cast<int*>(scratch + kWords);
+  int* wave_sum = reinterpret_cast<int*>(scratch + 2 * kWords);
+  const int n = max(last_key(w, tok0 + n_tok - 1) + 1 + (1 << a.s.shift) - 1, 0) >> a.s.shift;  // blocks there are to see
+  const int words = min((n + 31) / 32, kWords);
+  for (int i = tid; i < words; i += THREADS) marks[i] = 0;
+  __syncthreads();
+  const int total = n_tok * a.n_blocks;
+  const int32_t* ids = a.blocks + (static_cast<int64_t>(w.q0 + tok0) * a.kv_heads + kv_head) * a.n_blocks;
+  const int64_t to_next = static_cast<int64_t>(a.kv_heads) * a.n_blocks;
+  for (int i = tid; i < total; i += THREADS) {
+    const int t = i / a.n_blocks;
+    const int id = ids[t * to_next + i - t * a.n_blocks];
+    if (id >= 0 && id < 32 * words && (id << a.s.shift) <= last_key(w, tok0 + t)) atomicOr(&marks[id >> 5], 1u << (id & 31));
+  }
+  __syncthreads();
+  constexpr int kPer = kWords / THREADS;
+  int mine[kPer], local = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int at = tid * kPer + i;
+    mine[i] = at < words ? __popc(marks[at]) : 0;
+    local += mine[i];
+  }
+  const int incl = wave_incl_scan(local);
+  if ((tid & 63) == 63) wave_sum[tid >> 6] = incl;
+  __syncthreads();
+  int run = incl - local, all = 0;
+#pragma unroll
+  for (int i = 0; i < THREADS / 64; ++i) {
+    if (i < (tid >> 6)) run += wave_sum[i];
+    all += wave_sum[i];
+  }
+  ConstInts table = const_ints(a.s.table + w.seq * a.s.table_stride);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int at = tid * kPer + i;
+    if (at < words) below[at] = run;
+    if (mine[i] && run < lo + count && run + mine[i] > lo) {
+      uint32_t m = marks[at];
+      for (int r = run; m; ++r, m &= m - 1) {
+        if (r < lo || r >= lo + count) continue;
+        const int block = 32 * at + __ffs(m) - 1;
+        const int p = table[min(block, a.s.table_pages - 1)];
+        const bool ok = p >= 0 && p < a.s.n_pages;
+        list[r - lo].page = ok ? p : -1;
+        list[r - lo].block = block;
+        list[r - lo].tokens = n_tok == 1 && ok ? 1u : 0u;
+      }
+    }
+    run += mine[i];
+  }
+  __syncthreads();
+  if (n_tok > 1) {
+    for (int i = tid; i < total; i += THREADS) {
+      const int t = i / a.n_blocks;
+      const int id = ids[t * to_next + i - t * a.n_blocks];
+      if (id < 0 || id >= 32 * words || (id << a.s.shift) > last_key(w, tok0 + t)) continue;
+      const int r = below[id >> 5] + __popc(marks[id >> 5] & ((1u << (id & 31)) - 1)) - lo;
+      if (r >= 0 && r < count && list[r].page >= 0) atomicOr(&list[r].tokens, 1u << t);
+    }
+    __syncthreads();
+  }
+  return min(max(all - lo, 0), count);
+}
+
+// Where the token kernel's keys come from.
+enum Keys {
+  kTable,      // the table: the sequence's own keys
+  kListOne,    // listed blocks, tiles of one token
+  kListSeveral // listed blocks, tiles of several tokens, which see different blocks
+};
+
+template <int D, Keys KEYS>
+__global__ __launch_bounds__(64 * token_waves<D>(), 1) void paged_token_kernel(PagedArgs a) {
+  constexpr bool LISTED = KEYS != kTable;
+  constexpr int NW = token_waves<D>();
+  constexpr int kTile = kKeysT * 2 * D;
+  constexpr int kHalfOps = kTile / 2048;  // DMA instructions per half
+  // The stages are variables of their own: the compiler then knows that the
+  // DMA in flight into one does not write the other, and does not wait for it.
+  __shared__ __attribute__((aligned(1024))) uint8_t smem0[NW][2][kTile];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem1[NW][2][kTile];
+  __shared__ float s_m[NW][32], s_l[NW][32];
+  __shared__ ListEntry s_list[LISTED ? kList : 1];
+  static_assert(NW * 32 * D * 4 == sizeof(smem0), "the merge uses a stage");
+  static_assert(sizeof(smem0) >= 4 * (2 * kWords + 16), "and so does the list's scratch");
+  const int t_block = blockIdx.x / a.kv_heads, split = blockIdx.y;
+  // the heads of each sequence and split begin on another XCD
+  const int kv_head = (blockIdx.x + t_block + split) % a.kv_heads;
+  PagedTile w;
+  if (a.one_tile)
+    w.seq = t_block, w.tile = 0, w.tiles = 1;
+  else if (!find_tile(a, t_block, kRowsT, w))
+    return;
+  load_range(a, w);
+  const int r0 = w.tile * kRowsT, n_rows = min(w.lq, a.max_q) * a.group;
+  if (r0 >= n_rows) return;
+  const int here = min(n_rows - r0, kRowsT);  // rows of this tile
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int tok0 = r0 / a.group, tok1 = (r0 + here - 1) / a.group;
+  const LaneRow x = lane_row(a, w, kv_head, r0 + (lane & 31), n_rows);
+  const int lim_first = last_key(w, tok0);
+  const int slot = a.prefix_splits + split;
+  auto empty = [&](int at) {
+    if (wave == 0 && lane < here) empty_share(a, at, x.q_row, x.head);
+  };
+  if (a.every_slot() && a.slots > 1 && split == 0 && w.own == 0)
+    for (int i = 0; i < a.prefix_splits; ++i) empty(i);
+
+  int n_tiles, kbeg = 0, splits = 1, entries = 0;
+  if (LISTED) {
+    entries = uniform(build_list<64 * NW>(a, w, kv_head, tok0, tok1 - tok0 + 1, split * a.chunk, a.chunk, s_list,
+                                          reinterpret_cast<uint32_t*>(&smem0[0][0][0])));
+    n_tiles = ((entries << (a.s.shift - 4)) + 1) / 2;
+    if (n_tiles == 0 && a.slots > 1) return empty(slot);
+  } else {
+    const int all = max(last_key(w, tok1) + 1 - w.own, 0);
+    splits = (all + a.chunk - 1) / a.chunk;
+    if (split >= max(splits, a.every_slot() ? 0 : 1)) {
+      if (a.every_slot()) empty(slot);
+      return;
+    }
+    kbeg = w.own + split * a.chunk;
+    n_tiles = (min(all - split * a.chunk, a.chunk) + kKeysT - 1) / kKeysT;
+  }
+
+  bf16x8 q[D / 16];
+  load_q<D>(a, x, q);
+  const int slot_mask = (1 << a.s.shift) - 1;
+  ConstInts table = const_ints(a.s.table + w.seq * a.s.table_stride);
+  int koff[kHalfOps], voff[kHalfOps];
+#pragma unroll
+  for (int i = 0; i < kHalfOps; ++i) {
+    koff[i] = half_offset<D, false>(i, static_cast<int>(a.k.row_stride) * 2);
+    voff[i] = half_offset<D, true>(i, static_cast<int>(a.v.row_stride) * 2);
+  }
+  const uint32_t every = tok1 - tok0 == 31 ? ~0u : (2u << (tok1 - tok0)) - 1;
+  auto find = [&](int t, int hh) -> Half {
+    if (!LISTED) return table_half(a, table, kbeg + kKeysT * t + 16 * hh);
+    const int i = 2 * t + hh, e = i >> (a.s.shift - 4);
+    const ListEntry entry = s_list[min(e, entries - 1)];
+    const int page = uniform(entry.page), block = uniform(entry.block);
+    Half y;
+    y.page = max(page, 0);
+    y.key = (block << a.s.shift) + 16 * (i & (slot_mask >> 4));
+    y.visible = e < entries ? uniform(static_cast<int>(entry.tokens)) : 0u;
+    return y;
+  };
+  struct Pair {
+    Half h[2];
+  };
+  auto find_pair = [&](int t) { return Pair{{find(t, 0), find(t, 1)}}; };
+  auto issue = [&](uint8_t (&to)[2][kTile], const Pair& p) {
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const __amdgpu_buffer_rsrc_t kr = raw_buffer(half_base(a.k, p.h[hh], slot_mask, kv_head), 0x7fffffff);
+      const __amdgpu_buffer_rsrc_t vr = raw_buffer(half_base(a.v, p.h[hh], slot_mask, kv_head), 0x7fffffff);
+#pragma unroll
+      for (int i = 0; i < kHalfOps; ++i) dma16(kr, koff[i], 0, &to[0][1024 * (kHalfOps * hh + i)]);
+#pragma unroll
+      for (int i = 0; i < kHalfOps; ++i) dma16(vr, voff[i], 0, &to[1][1024 * (kHalfOps * hh + i)]);
+    }
+  };
+
+  RowState<D> st;
+  st.clear();
+  Pair now, next;
+  // Tile t is in one stage; the reads of the other have returned: refill it.
+  auto turn = [&](uint8_t (&to)[2][kTile], int t) {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), other counters untouched
+    if (t + NW < n_tiles) {
+      next = find_pair(t + NW);
+      issue(to, next);
+      wait_vmcnt<4 * kHalfOps>();
+    } else {
+      wait_vmcnt<0>();
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // whether every row sees all of the tile
+  auto whole = [&](const Pair& p) {
+    return p.h[0].key + 15 <= lim_first && p.h[1].key + 15 <= lim_first &&
+           (p.h[0].visible & p.h[1].visible & every) == every;
+  };
+  const int tk = static_cast<int>(x.q_row) - w.q0 - tok0;  // the lane's token
+  auto masked = [&](const uint8_t (&from)[2][kTile], int t) {
+    Limits<1> lim;
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh)
+      lim.at[hh] = (now.h[hh].visible >> tk) & 1 ? x.limit - now.h[hh].key + 16 * hh : -1;
+    attend_halves<D, 1>(from[0], from[1], q, st, a.c, lim, a.v.row_stride,
+                        [&](int i) { return half_base(a.v, find(t, i), slot_mask, kv_head); });
+  };
+  int t = wave;
+  if (t < n_tiles) {
+    now = find_pair(t);
+    issue(smem0[wave], now);
+  }
+  if (KEYS == kListSeveral) {
+    for (; t < n_tiles; t += 2 * NW) {
+      turn(smem1[wave], t);
+      masked(smem0[wave], t);
+      now = next;
+      if (t + NW >= n_tiles) break;
+      turn(smem0[wave], t + NW);
+      masked(smem1[wave], t + NW);
+      now = next;
+    }
+  } else {
+    // tiles that every row sees whole, in pairs; the rest
+    int stage = 0;
+    while (t < n_tiles && whole(now)) {
+      turn(smem1[wave], t);
+      attend<D, 1, false>(smem0[wave][0], smem0[wave][1], q, st, a.c, 0, false);
+      now = next;
+      t += NW;
+      stage = 1;
+      if (t >= n_tiles || !whole(now)) break;
+      turn(smem0[wave], t);
+      attend<D, 1, false>(smem1[wave][0], smem1[wave][1], q, st, a.c, 0, false);
+      now = next;
+      t += NW;
+      stage = 0;
+    }
+    for (; t < n_tiles; t += NW, stage ^= 1) {
+      uint8_t(&from)[2][kTile] = stage ? smem1[wave] : smem0[wave];
+      turn(stage ? smem0[wave] : smem1[wave], t);
+      masked(from, t);
+      now = next;
+    }
+  }
+  __syncthreads();
+
+  // the merge: quad d of row r of a wave is at slot d ^ (r mod 16), off the other rows' banks
+  auto merge = [&](int wv, int r, int quad) {
+    return reinterpret_cast<f32x4*>(&smem0[0][0][0]) + (wv * 32 + r) * (D / 4) + (quad ^ (r & 15));
+  };
+  const int n = lane & 31, h = lane >> 5;
+  const float lsum = sum_halves(st.l);
+  if (n < here) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *merge(wave, n, 8 * i + 2 * j + h) =
+            f32x4{st.o[i][4 * j], st.o[i][4 * j + 1], st.o[i][4 * j + 2], st.o[i][4 * j + 3]};
+    if (h == 0) s_m[wave][n] = st.m, s_l[wave][n] = lsum;
+  }
+  __syncthreads();
+  const bool direct = a.every_slot() ? a.slots == 1 : splits <= 1;
+  for (int u = threadIdx.x; u < here * (D / 4); u += 64 * NW) {
+    const int r = u / (D / 4), d = 4 * (u % (D / 4));
+    float m = kNegInf, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) m = fmaxf(m, s_m[i][r]);
+    const float ms = m == kNegInf ? 0.f : m;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const float f = __builtin_amdgcn_exp2f((s_m[i][r] - ms) * a.c);
+      l += f * s_l[i][r];
+      o += f * *merge(i, r, d / 4);
+    }
+    const int pos = (r0 + r) / a.group;
+    const int64_t q_row = w.q0 + pos;
+    const int head = kv_head * a.group + r0 + r - pos * a.group;
+    if (direct) {
+      store_quad(a, q_row, head, d, o, m, l);
+    } else {
+      const int64_t row = part_row(a, slot, q_row, head);
+      *reinterpret_cast<f32x4*>(a.part_o + row * D + d) = o;
+      if (d == 0) a.part_ml[row] = make_float2(m, l);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- many rows
+constexpr int kRowsP = 128;  // rows of a block: 4 waves x 32
+constexpr int kKeysP = 64;   // keys of a tile
+
+template <int D, bool PREFIX>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(PagedArgs a) {
+  constexpr int kTile = kKeysP * 2 * D;
+  constexpr int kOps = kTile / 4096;  // DMA instructions per wave and tile
+  // two variables: see paged_token_kernel
+  __shared__ __attribute__((aligned(1024))) uint8_t smem0[2][kTile];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem1[2][kTile];
+  const int kv_head = blockIdx.x % a.kv_heads, split = blockIdx.y;
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  PagedTile w;
+  LaneRow x;
+  // the last key that some row of the wave sees; the last that every row of the block sees; keys of the block
+  int lim_last, block_first, all;
+  if (PREFIX) {
+    GroupRange g;
+    if (!find_group_tile(a, blockIdx.x / a.kv_heads, kRowsP, w, g)) return;
+    x = lane_row(a, w, kv_head, w.tile * kRowsP + 32 * wave + (lane & 31), w.lq * a.group);
+    // the row's sequence: the last one that begins at or before it
+    int lo = g.first, hi = g.past;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (a.s.cu_q[mid] <= x.q_row) lo = mid; else hi = mid;
+    }
+    const PagedRange s = sequence(a, lo, 0);
+    const int pos = static_cast<int>(x.q_row) - s.q0;
+    x.limit = min(pos + s.diag, w.end - 1);
+    if (pos < 0 || pos >= min(s.lq, a.max_q)) x.valid = false, x.limit = w.end - 1;
+    block_first = lim_last = x.limit;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      block_first = min(block_first, __shfl_xor(block_first, off, 64));
+      lim_last = max(lim_last, __shfl_xor(lim_last, off, 64));
+    }
+    lim_last = uniform(lim_last);
+    __shared__ int s_first[4];
+    if (lane == 0) s_first[wave] = block_first;
+    __syncthreads();
+    block_first = uniform(min(min(s_first[0], s_first[1]), min(s_first[2], s_first[3])));
+    all = w.end;
+  } else {
+    if (!find_tile(a, blockIdx.x / a.kv_heads, kRowsP, w)) return;
+    load_range(a, w);
+    const int r0 = (w.tiles - 1 - w.tile) * kRowsP;  // the last tiles see the most keys: first
+    const int n_rows = min(w.lq, a.max_q) * a.group, rw = r0 + 32 * wave;
+    x = lane_row(a, w, kv_head, rw + (lane & 31), n_rows);
+    block_first = last_key(w, r0 / a.group);
+    lim_last = last_key(w, min(rw + 31, n_rows - 1) / a.group);
+    all = max(last_key(w, (min(r0 + kRowsP, n_rows) - 1) / a.group) + 1 - w.own, 0);
+  }
+  const int chunk = PREFIX ? a.prefix_chunk : a.chunk;
+  const int slot = PREFIX ? split : a.prefix_splits + split;
+  const int splits = (all + chunk - 1) / chunk;  // that have keys to see
+  auto empty = [&](int at) {
+    if (x.valid && lane < 32) empty_share(a, at, x.q_row, x.head);
+  };
+  if (!PREFIX && a.n_groups > 0 && split == 0 && w.own == 0)
+    for (int i = 0; i < a.prefix_splits; ++i) empty(i);
+  if (split >= max(splits, a.n_groups > 0 ? 0 : 1)) {
+    if (a.n_groups > 0) empty(slot);
+    return;
+  }
+  const int kbeg = w.own + split * chunk, kend = kbeg + min(all - split * chunk, chunk);
+
+  bf16x8 q[D / 16];
+  load_q<D>(a, x, q);
+  const int slot_mask = (1 << a.s.shift) - 1;
+  ConstInts table = const_ints(a.s.table + w.seq * a.s.table_stride);
+  // instruction i of a wave fills rows from (4 i + wave) * 512 / D on: one half each
+  constexpr int kRowsOp = 512 / D;
+  constexpr int kSame = D == 256 ? 2 : 1;  // instructions of a wave in a half
+  const int in_half = D == 256 ? 0 : D == 128 ? wave : wave & 1;  // place of instruction 0 in its half
+  int koff[kSame], voff[kSame];
+#pragma unroll
+  for (int i = 0; i < kSame; ++i) {
+    koff[i] = half_offset<D, false>(D == 256 ? 4 * i + wave : in_half, static_cast<int>(a.k.row_stride) * 2);
+    voff[i] = half_offset<D, true>(D == 256 ? 4 * i + wave : in_half, static_cast<int>(a.v.row_stride) * 2);
+  }
+  struct Quad {
+    Half h[4];
+  };
+  auto find_quad = [&](int key) {
+    return Quad{{table_half(a, table, key), table_half(a, table, key + 16), table_half(a, table, key + 32),
+                 table_half(a, table, key + 48)}};
+  };
+  auto issue = [&](uint8_t (&to)[2][kTile], const Quad& p) {
+#pragma unroll
+    for (int i = 0; i < kOps; ++i) {
+      // row (4 i + wave) * kRowsOp of the tile
+      Half y = p.h[4 * i * kRowsOp / 16];
+      if (D == 64 && wave >= 2) y = p.h[4 * i * kRowsOp / 16 + 1];
+      const __amdgpu_buffer_rsrc_t kr = raw_buffer(half_base(a.k, y, slot_mask, kv_head), 0x7fffffff);
+      const __amdgpu_buffer_rsrc_t vr = raw_buffer(half_base(a.v, y, slot_mask, kv_head), 0x7fffffff);
+      dma16(kr, koff[i % kSame], 0, &to[0][1024 * (4 * i + wave)]);
+      dma16(vr, voff[i % kSame], 0, &to[1][1024 * (4 * i + wave)]);
+    }
+  };
+
+  RowState<D> st;
+  st.clear();
+  Quad now, next;
+  // Tile `key` has arrived in one stage and every wave is done with the other: refill that.
+  auto turn = [&](uint8_t (&to)[2][kTile], int key) {
+    wait_vmcnt<0>();
+    stage_barrier();
+    if (key + kKeysP < kend) {
+      next = find_quad(key + kKeysP);
+      issue(to, next);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto valid = [&](const Quad& p) {
+    return (p.h[0].visible & p.h[1].visible & p.h[2].visible & p.h[3].visible) != 0;
+  };
+  int key = kbeg, stage = 0;
+  if (key < kend) {
+    now = find_quad(key);
+    issue(smem0, now);
+  }
+  // tiles that every row of the block sees whole, in pairs
+  const int full = min(kend, block_first + 1);
+  while (key + kKeysP <= full && valid(now)) {
+    turn(smem1, key);
+    attend<D, kKeysP / 32, false>(smem0[0], smem0[1], q, st, a.c, 0, false);
+    now = next;
+    key += kKeysP;
+    stage = 1;
+    if (key + kKeysP > full || !valid(now)) break;
+    turn(smem0, key);
+    attend<D, kKeysP / 32, false>(smem1[0], smem1[1], q, st, a.c, 0, false);
+    now = next;
+    key += kKeysP;
+    stage = 0;
+  }
+  // the rest
+  for (; key < kend; key += kKeysP, stage ^= 1) {
+    uint8_t(&from)[2][kTile] = stage ? smem1 : smem0;
+    turn(stage ? smem0 : smem1, key);
+    if (key <= lim_last) {
+      Limits<kKeysP / 32> lim;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lim.at[i] = now.h[i].visible ? x.limit - key : -1;
+      attend_halves<D, kKeysP / 32>(from[0], from[1], q, st, a.c, lim, a.v.row_stride, [&](int i) {
+        return half_base(a.v, table_half(a, table, key + 16 * i), slot_mask, kv_head);
+      });
+    }
+    now = next;
+  }
+
+  const float l = sum_halves(st.l);
+  if (!x.valid) return;
+  const int h = lane >> 5;
+  const bool direct = a.n_groups == 0 && splits <= 1;
+  const int64_t row = part_row(a, slot, x.q_row, x.head);
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // register 4 j + e of o[i] is output 32 i + 8 j + 4 h + e
+      const f32x4 o = {st.o[i][4 * j], st.o[i][4 * j + 1], st.o[i][4 * j + 2], st.o[i][4 * j + 3]};
+      const int d = 32 * i + 8 * j + 4 * h;
+      if (direct)
+        store_quad(a, x.q_row, x.head, d, o, st.m, l);
+      else
+        *reinterpret_cast<f32x4*>(a.part_o + row * D + d) = o;
+    }
+  if (!direct && h == 0) a.part_ml[row] = make_float2(st.m, l);
+}
+
+// ---------------------------------------------------------------- the join of the shares
+// A thread per four outputs of a row, kJoin shares at a time, so that their latencies
+// overlap; with more than kJoinShared slots the block has one row, and its thread groups
+// take turns over them and meet in LDS.  Either way in a fixed order.
+constexpr int kJoin = 8, kJoinShared = 2 * kJoin;
+template <int D>
+__global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a) {
+  constexpr int kGroups = 256 / (D / 4);
+  __shared__ f32x4 s_o[kGroups][D / 4];
+  __shared__ float2 s_ml[kGroups];
+  const int grp = threadIdx.x / (D / 4), quad = threadIdx.x % (D / 4);
+  const bool shared = a.join_rows == 1;
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * a.join_rows + (shared ? 0 : grp);
+  int64_t q_row = u / a.q_heads;
+  const int head = static_cast<int>(u - q_row * a.q_heads);
+  int seq, pos;
+  if (a.one_tile) {  // u counts the rows below max_q of each sequence
+    seq = static_cast<int>(q_row / a.max_q);
+    if (seq >= a.s.n_seqs) return;
+    pos = static_cast<int>(q_row - static_cast<int64_t>(seq) * a.max_q);
+  } else {  // u counts q's rows: the sequence is the last one that begins at or before it
+    if (q_row >= a.s.q_rows) return;
+    int lo = 0, hi = a.s.n_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (a.s.cu_q[mid] <= q_row) lo = mid; else hi = mid;
+    }
+    seq = lo;
+    pos = 0;
+  }
+  const PagedRange w = sequence(a, seq, 0);
+  if (a.one_tile)
+    q_row = w.q0 + pos;
+  else
+    pos = static_cast<int>(q_row) - w.q0;
+  if (pos < 0 || pos >= min(w.lq, a.max_q)) return;
+  int splits = a.slots;
+  if (!a.every_slot()) {
+    // The tile kernels cut by what the tile's last row sees.
+    const int last = min((pos * a.group + head % a.group) / a.tile_rows * a.tile_rows + a.tile_rows,
+                         min(w.lq, a.max_q) * a.group) - 1;
+    splits = (max(last_key(w, last / a.group) + 1, 0) + a.chunk - 1) / a.chunk;
+    if (splits <= 1) return;  // written by its tile
+  }
+  float m = kNegInf, l = 0.f;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  // a share (ml, p) with weight 2^((its maximum - m) c)
+  auto rescale = [&](float to) {
+    const float f = m == to ? 1.f : __builtin_amdgcn_exp2f((m - to) * a.c);
+    m = to;
+    l *= f;
+    o *= f;
+  };
+  auto add = [&](float2 ml, f32x4 p) {
+    const float f = __builtin_amdgcn_exp2f((ml.x - (m == kNegInf ? 0.f : m)) * a.c);
+    l += f * ml.y;
+    o += f * p;
+  };
+  const int step = shared ? kGroups : 1;
+  for (int i = shared ? grp : 0; i < splits; i += kJoin * step) {
+    float2 ml[kJoin];
+    f32x4 part[kJoin];
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j) {
+      ml[j] = make_float2(kNegInf, 0.f);
+      if (i + j * step < splits) ml[j] = a.part_ml[part_row(a, i + j * step, q_row, head)];
+    }
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j) {
+      part[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (ml[j].y != 0.f)  // a slot without keys has no output
+        part[j] = *reinterpret_cast<const f32x4*>(a.part_o + part_row(a, i + j * step, q_row, head) * D + 4 * quad);
+    }
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j) top = fmaxf(top, ml[j].x);
+    rescale(top);
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j) add(ml[j], part[j]);
+  }
+  if (shared) {  // the whole block is here: it has one row
+    s_o[grp][quad] = o;
+    if (quad == 0) s_ml[grp] = make_float2(m, l);
+    __syncthreads();
+    if (grp != 0) return;
+    float top = m;
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) top = fmaxf(top, s_ml[g].x);
+    rescale(top);
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) add(s_ml[g], s_o[g][quad]);
+  }
+  store_quad(a, q_row, head, 4 * quad, o, m, l);
+}
+
+// ---------------------------------------------------------------- host
+constexpr int kCus = 256;
+constexpr int kRounds = 64;
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Plan {
+  bool token, one_tile;
+  int64_t tiles, prefix_tiles;  // row tiles x key heads
+  int chunk, splits;            // of the own keys (listed blocks)
+  int prefix_chunk, prefix_splits;
+  int slots() const { return splits + prefix_splits; }
+};
+
+// Tokens that a tile of the token kernel may hold rows of.
+int tile_tokens(int group, int max_q) {
+  const int n = kRowsT % group == 0 ? kRowsT / group : group % kRowsT == 0 ? 1 : (kRowsT - 2) / group + 2;
+  return std::min(n, max_q);
+}
+
+// Keys of a block for `tiles` tiles over `keys` keys: enough blocks to fill the card,
+// pieces not so small that their join costs more than it gains.
+int64_t pick_chunk(int64_t keys, int64_t tiles, int64_t unit, int64_t want, int64_t least, int64_t most) {
+  int64_t chunk = ceil_div(keys, std::max<int64_t>(1, ceil_div(want, std::max<int64_t>(tiles, 1))));
+  chunk = std::min(std::max(chunk, least), most);
+  return ceil_div(chunk, unit) * unit;
+}
+
+Plan make_plan(const moe_paged_attn& d) {
+  Plan p = {};
+  const moe_paged& s = d.p;
+  const int64_t g = s.q_heads / s.kv_heads;
+  const int64_t seqs = std::min<int64_t>(s.n_seqs, s.q_rows);
+  const bool listed = d.n_blocks > 0, grouped = d.n_groups > 0;
+  p.one_tile = d.max_q * g <= kRowsT;
+  p.token = p.one_tile || listed;
+  p.tiles = (p.one_tile ? s.n_seqs : seqs + s.q_rows * g / (p.token ? kRowsT : kRowsP)) * s.kv_heads;
+  const int64_t tiles = std::max<int64_t>(p.tiles, 1);
+  int64_t keys = std::max(d.max_kv, 1);
+  if (grouped) keys += s.page_size - 1;  // what is left of the prefix's last page
+  if (listed)
+    keys = std::max<int64_t>(1, std::min<int64_t>(static_cast<int64_t>(tile_tokens(g, d.max_q)) * d.n_blocks,
+                                                  ceil_div(keys, s.page_size))) * s.page_size;
+  const int64_t unit = p.token ? kKeysT * (s.head_dim == 256 ? 2 : 4) : kKeysP;
+  const int64_t want = s.head_dim > (p.token ? 64 : 128) ? kCus : 2 * kCus;
+  const int64_t least = p.token ? (keys <= 4 * unit ? 4 : 2) * unit
+                                : std::min(std::max(tiles / 16, int64_t{4}), int64_t{16}) * unit;
+  const int64_t most = !p.token ? INT32_MAX
+                                : std::max(16 * unit, ceil_div(keys, std::max(kRounds * kCus / tiles, int64_t{1})));
+  const int64_t chunk = pick_chunk(keys, p.tiles, unit, want, least, most);
+  if (listed) {
+    p.chunk = static_cast<int>(std::min<int64_t>(ceil_div(chunk, s.page_size), kList));
+    p.splits = static_cast<int>(ceil_div(keys / s.page_size, p.chunk));
+  } else {
+    p.chunk = static_cast<int>(std::min<int64_t>(chunk, 1 << 30));
+    p.splits = static_cast<int>(ceil_div(keys, chunk));
+  }
+  if (grouped && d.max_prefix >= s.page_size) {
+    p.prefix_tiles = (std::min<int64_t>(d.n_groups, s.q_rows) + s.q_rows * g / kRowsP) * s.kv_heads;
+    const int64_t piece = pick_chunk(d.max_prefix, p.prefix_tiles, kKeysP, s.head_dim > 128 ? kCus : 2 * kCus,
+                                     std::min(std::max(p.prefix_tiles / 16, int64_t{4}), int64_t{16}) * kKeysP, 1 << 30);
+    p.prefix_chunk = static_cast<int>(piece);
+    p.prefix_splits = static_cast<int>(ceil_div(d.max_prefix, piece));
+  }
+  return p;
+}
+
+inline size_t align256(size_t v) { return (v + 255) & ~size_t{255}; }
+
+size_t part_bytes(const moe_paged_attn& d, const Plan& p) {
+  if (p.slots() <= 1) return 0;
+  const size_t rows = static_cast<size_t>(p.slots()) * d.p.q_rows * d.p.q_heads;
+  return align256(rows * d.p.head_dim * 4) + align256(rows * 8);
+}
+
+// The shape fields, which the workspace depends on.
+int check_shape(const moe_paged_attn* a) {
+  if (!a) return MOE_EINVAL;
+  const int st = check_paged_shape(a->p, false);
+  if (st != MOE_OK) return st;
+  const int64_t capacity = static_cast<int64_t>(a->p.table_pages) * a->p.page_size;
+  if (a->max_q < 0 || a->max_q > a->p.q_rows || a->max_kv < 0 || a->max_kv > capacity) return MOE_EINVAL;
+  if (a->max_prefix < 0 || a->max_prefix > capacity || a->n_groups < 0 || a->n_groups > a->p.n_seqs) return MOE_EINVAL;
+  if (a->n_blocks < 0 || (a->n_blocks > 0 && a->n_groups > 0)) return MOE_EINVAL;
+  if (a->n_blocks > 1024) return MOE_ESHAPE;
+  if (a->n_blocks > 0 && a->max_kv > static_cast<int64_t>(32 * kWords) * a->p.page_size) return MOE_ESHAPE;
+  const Plan p = make_plan(*a);
+  // grid limits: 2^32 threads along x, 65535 blocks along y
+  if (p.tiles > 0xffffff || p.prefix_tiles > 0xffffff || p.splits > 65535 || p.prefix_splits > 65535) return MOE_ESHAPE;
+  if (static_cast<int64_t>(a->p.q_rows) * a->p.q_heads > 0x3fffffff) return MOE_ESHAPE;
+  return MOE_OK;
+}
+
+template <int D>
+void launch(const PagedArgs& a, const Plan& p, hipStream_t s) {
+  if (p.prefix_splits)
+    paged_rows_kernel<D, true><<<dim3(static_cast<unsigned>(p.prefix_tiles), static_cast<unsigned>(p.prefix_splits)),
+                                 256, 0, s>>>(a);
+  const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>(p.splits));
+  if (a.n_blocks && tile_tokens(a.group, a.max_q) == 1)
+    paged_token_kernel<D, kListOne><<<grid, 64 * token_waves<D>(), 0, s>>>(a);
+  else if (a.n_blocks)
+    paged_token_kernel<D, kListSeveral><<<grid, 64 * token_waves<D>(), 0, s>>>(a);
+  else if (p.token)
+    paged_token_kernel<D, kTable><<<grid, 64 * token_waves<D>(), 0, s>>>(a);
+  else
+    paged_rows_kernel<D, false><<<grid, 256, 0, s>>>(a);
+  if (a.slots > 1) {
+    const int64_t rows = (a.one_tile ? static_cast<int64_t>(a.s.n_seqs) * a.max_q : a.s.q_rows) * a.q_heads;
+    paged_join_kernel<D><<<static_cast<unsigned>(ceil_div(rows, a.join_rows)), 256, 0, s>>>(a);
+  }
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+size_t moe_paged_attention_workspace_size(const moe_paged_attn* a) {
+  if (moe::check_shape(a) != MOE_OK || a->p.n_seqs == 0 || a->p.q_rows == 0 || a->max_q == 0) return 0;
+  return moe::part_bytes(*a, moe::make_plan(*a));
+}
+
+int moe_paged_attention(const moe_paged_attn* a, void* ws, size_t ws_bytes, void* stream) {
+  int st = moe::check_shape(a);
+  if (st != MOE_OK) return st;
+  if (!(a->scale > 0.f && a->scale <= 0x1p127f)) return MOE_EINVAL;  // scale * log2(e) is finite
+  const moe_paged& p = a->p;
+  if (p.n_seqs == 0 || p.q_rows == 0 || a->max_q == 0) return MOE_OK;
+  if ((st = moe::check_paged_arrays(p)) != MOE_OK) return st;
+  if (a->n_groups > 0 && (!a->cu_group || !a->prefix_len)) return MOE_EINVAL;
+  if (a->n_blocks > 0 && !a->blocks) return MOE_EINVAL;
+  for (const moe_heads* h : {&a->q, &a->out})
+    if ((st = moe::check_paged_heads(*h)) != MOE_OK) return st;
+  if (p.n_pages > 0)
+    for (const moe_pages* h : {&a->k, &a->v})
+      if ((st = moe::check_pages(*h)) != MOE_OK) return st;
+  const moe::Plan plan = moe::make_plan(*a);
+  const size_t need = moe::part_bytes(*a, plan);
+  if (need) {
+    if (!ws) return MOE_EINVAL;
+    if (reinterpret_cast<uintptr_t>(ws) & 255) return MOE_EALIGN;
+    if (ws_bytes < need) return MOE_EWORKSPACE;
+  }
+  moe::PagedArgs k;
+  k.s = moe::paged_seqs(p);
+  k.q = a->q, k.out = a->out, k.k = a->k, k.v = a->v;
+  k.cu_group = a->cu_group, k.prefix_len = a->prefix_len, k.blocks = a->blocks, k.lse = a->lse;
+  k.part_o = static_cast<float*>(ws);
+  const size_t rows = static_cast<size_t>(plan.slots()) * p.q_rows * p.q_heads;
+  k.part_ml =
+      need ? reinterpret_cast<float2*>(static_cast<char*>(ws) + moe::align256(rows * p.head_dim * 4)) : nullptr;
+  k.q_heads = p.q_heads, k.kv_heads = p.kv_heads, k.group = p.q_heads / p.kv_heads;
+  k.max_q = a->max_q, k.n_groups = a->n_groups, k.n_blocks = a->n_blocks;
+  k.max_kv = std::min(a->max_kv, k.s.capacity), k.max_prefix = std::min(a->max_prefix, k.s.capacity);
+  k.chunk = plan.chunk, k.prefix_chunk = plan.prefix_chunk, k.prefix_splits = plan.prefix_splits;
+  k.slots = plan.slots();
+  k.one_tile = plan.one_tile, k.token = plan.token;
+  k.tile_rows = plan.token ? moe::kRowsT : moe::kRowsP;
+  k.join_rows = plan.slots() > moe::kJoinShared ? 1 : 256 / (p.head_dim / 4);
+  k.scale = a->scale;
+  k.c = a->scale * 1.44269504088896340736f;  // log2(e)
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  switch (p.head_dim) {
+    case 64: moe::launch<64>(k, plan, s); break;
+    case 128: moe::launch<128>(k, plan, s); break;
+    default: moe::launch<256>(k, plan, s); break;
+  }
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+}  // extern "C"
