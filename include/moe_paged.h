@@ -191,7 +191,12 @@ typedef struct moe_select {
   int32_t* blocks;        /* out */
 } moe_select;
 
+/* Depends on the shape fields only (kv_heads, n_seqs, q_rows, page_size, max_q, max_kv); 0 for a shape
+ * that needs none or is not supported. */
 size_t moe_select_blocks_workspace_size(const moe_select* a);
+
+/* ws: at least that many bytes, 256-byte aligned (may be NULL when that is 0).  q_rows * kv_heads < 2^23
+ * (MOE_ESHAPE otherwise). */
 int moe_select_blocks(const moe_select* a, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus

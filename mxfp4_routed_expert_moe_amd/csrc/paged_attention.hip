@@ -34,11 +34,10 @@ struct PagedArgs {
   float* part_o;    // [slots, q_rows, q_heads, D]
   float2* part_ml;  // [slots, q_rows, q_heads]: maximum, sum
   int q_heads, kv_heads, group, max_q, max_kv, n_groups, max_prefix, n_blocks;
-  int chunk;         // own keys (listed blocks) of a split
+  int chunk, splits; // own keys of a split (listed blocks: the fewest), and how many there are at most
   int prefix_chunk;  // prefix keys of a split
   int prefix_splits, slots;
-  int one_tile;      // every sequence is one tile of the token kernel
-  int token;         // the token kernel did the own keys
+  int token;         // the token kernel did the own keys: every sequence is one tile of it
   int tile_rows;     // rows of a tile of the kernel that did the own keys
   int join_rows;     // rows of a block of the join
   float scale, c;    // c = scale * log2(e)
@@ -178,11 +177,12 @@ __device__ __forceinline__ void empty_share(const PagedArgs& a, int slot, int64_
 
 // A tile whose rows see some of its 16-key halves only, or none: as attend_masked of the
 // contiguous kernels, with a limit per half; row(i): the values of half i's first key.
+// scan = false: every value of the tile is taken for finite.
 template <int D, int NT, typename Row>
 __device__ __forceinline__ void attend_halves(const uint8_t* ks, const uint8_t* vs, const bf16x8 (&q)[D / 16],
-                                              RowState<D>& st, float c, const Limits<NT>& lim, int64_t row_stride,
-                                              Row row) {
-  const bool dirty = any_not_finite(vs, NT * 32 * 2 * D);
+                                              RowState<D>& st, float c, const Limits<NT>& lim, bool scan,
+                                              int64_t row_stride, Row row) {
+  const bool dirty = scan && any_not_finite(vs, NT * 32 * 2 * D);
   attend<D, NT, true>(ks, vs, q, st, c, lim, dirty);
   if (!dirty) return;
   const int h = (threadIdx.x & 63) >> 5;
@@ -204,6 +204,17 @@ __device__ __forceinline__ int half_offset(int i, int row_bytes) {
   const int lane = threadIdx.x & 63;
   const int r = i * (64 / kChunks) + lane / kChunks, s = lane % kChunks;
   return r * row_bytes + 16 * (VALUE ? v_slot<D>(r, s) : k_slot<D>(r, s));
+}
+
+// Whether an output of the wave is not finite.
+template <int D>
+__device__ __forceinline__ bool not_finite(const RowState<D>& st) {
+  float zero = 0.f;  // 0 times what is finite
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) zero = __builtin_fmaf(st.o[i][j], 0.f, zero);
+  return __any(zero != 0.f);
 }
 
 // Sixteen keys: where they are, and the position of the first.
@@ -235,24 +246,29 @@ constexpr int kWords = 1024;  // 32-block words of the marks: blocks per sequenc
 template <int D>
 constexpr int token_waves() { return D == 256 ? 2 : 4; }
 
-// The listed blocks of a tile's tokens, each once and ascending: entries lo .. lo +
-// count - 1 of that list.  An entry is a page, its block and the tokens that list it.
+// The listed blocks of a tile's tokens, each once and ascending, of which the splits
+// take equal shares (as many as `least` there are, or less in the last).  An entry is a
+// page (-1: none), its block, and for each 32 rows of the tile the tokens that list it,
+// from the first of those rows on.
+template <int PARTS>
 struct ListEntry {
   int page, block;
-  uint32_t tokens;
+  uint32_t tokens[PARTS];
 };
 
 // Marks are set with integer atomics (their order changes nothing) in LDS, one bit a
 // block; a block's place in the list is the number of marks below it.  scratch: at
-// least 2 * kWords + 16 ints.  Returns the entries from lo on, at most `count`.
-template <int THREADS>
-__device__ int build_list(const PagedArgs& a, const PagedTile& w, int kv_head, int tok0, int n_tok, int lo, int count,
-                          ListEntry* list, uint32_t* scratch) {
+// least 2 * kWords + 16 ints; r0: the tile's first row, rows: its rows.  Returns the number of
+// entries of this split's share (at most kList: the plan sees to it).
+template <int THREADS, int PARTS>
+__device__ int build_list(const PagedArgs& a, const PagedTile& w, int kv_head, int r0, int rows, int split,
+                          ListEntry<PARTS>* list, uint32_t* scratch) {
   const int tid = threadIdx.x;
   uint32_t* marks = scratch;
   int* below = reinterpret_cast<int*>(scratch + kWords);
   int* wave_sum = reinterpret_cast<int*>(scratch + 2 * kWords);
-  const int n = max(last_key(w, tok0 + n_tok - 1) + 1 + (1 << a.s.shift) - 1, 0) >> a.s.shift;  // blocks there are to see
+  const int tok0 = r0 / a.group, n_tok = (r0 + rows - 1) / a.group - tok0 + 1;
+  const int n = (max(last_key(w, tok0 + n_tok - 1), -1) >> a.s.shift) + 1;  // blocks there are to see
   const int words = min((n + 31) / 32, kWords);
   for (int i = tid; i < words; i += THREADS) marks[i] = 0;
   __syncthreads();
@@ -282,7 +298,8 @@ __device__ int build_list(const PagedArgs& a, const PagedTile& w, int kv_head, i
     if (i < (tid >> 6)) run += wave_sum[i];
     all += wave_sum[i];
   }
-  ConstInts table = const_ints(a.s.table + w.seq * a.s.table_stride);
+  const int count = min(max((all + a.splits - 1) / a.splits, a.chunk), kList), lo = split * count;
+  const int32_t* table = a.s.table + w.seq * a.s.table_stride;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int at = tid * kPer + i;
@@ -296,7 +313,8 @@ __device__ int build_list(const PagedArgs& a, const PagedTile& w, int kv_head, i
         const bool ok = p >= 0 && p < a.s.n_pages;
         list[r - lo].page = ok ? p : -1;
         list[r - lo].block = block;
-        list[r - lo].tokens = n_tok == 1 && ok ? 1u : 0u;
+#pragma unroll
+        for (int j = 0; j < PARTS; ++j) list[r - lo].tokens[j] = n_tok == 1 && ok ? 1u : 0u;
       }
     }
     run += mine[i];
@@ -308,11 +326,28 @@ __device__ int build_list(const PagedArgs& a, const PagedTile& w, int kv_head, i
       const int id = ids[t * to_next + i - t * a.n_blocks];
       if (id < 0 || id >= 32 * words || (id << a.s.shift) > last_key(w, tok0 + t)) continue;
       const int r = below[id >> 5] + __popc(marks[id >> 5] & ((1u << (id & 31)) - 1)) - lo;
-      if (r >= 0 && r < count && list[r].page >= 0) atomicOr(&list[r].tokens, 1u << t);
+      if (r < 0 || r >= count || list[r].page < 0) continue;
+#pragma unroll
+      for (int j = 0; j < PARTS; ++j) {
+        const int from = (r0 + 32 * j) / a.group - tok0, to = (r0 + 32 * j + 31) / a.group - tok0;
+        if (t >= from && t <= to) atomicOr(&list[r].tokens[j], 1u << (t - from));
+      }
     }
     __syncthreads();
   }
   return min(max(all - lo, 0), count);
+}
+
+// Half i of a list: the 16 keys at i % (page_size / 16) of entry i / (page_size / 16).
+template <int PARTS>
+__device__ __forceinline__ Half list_half(const PagedArgs& a, const ListEntry<PARTS>* list, int entries, int i, int part) {
+  const int e = i >> (a.s.shift - 4);
+  const ListEntry<PARTS>& entry = list[min(e, entries - 1)];
+  Half x;
+  x.page = max(uniform(entry.page), 0);
+  x.key = (uniform(entry.block) << a.s.shift) + 16 * (i & ((1 << (a.s.shift - 4)) - 1));
+  x.visible = e < entries ? static_cast<uint32_t>(uniform(static_cast<int>(entry.tokens[part]))) : 0u;
+  return x;
 }
 
 // Where the token kernel's keys come from.
@@ -333,21 +368,18 @@ __global__ __launch_bounds__(64 * token_waves<D>(), 1) void paged_token_kernel(P
   __shared__ __attribute__((aligned(1024))) uint8_t smem0[NW][2][kTile];
   __shared__ __attribute__((aligned(1024))) uint8_t smem1[NW][2][kTile];
   __shared__ float s_m[NW][32], s_l[NW][32];
-  __shared__ ListEntry s_list[LISTED ? kList : 1];
+  __shared__ ListEntry<1> s_list[LISTED ? kList : 1];
   static_assert(NW * 32 * D * 4 == sizeof(smem0), "the merge uses a stage");
   static_assert(sizeof(smem0) >= 4 * (2 * kWords + 16), "and so does the list's scratch");
   const int t_block = blockIdx.x / a.kv_heads, split = blockIdx.y;
   // the heads of each sequence and split begin on another XCD
   const int kv_head = (blockIdx.x + t_block + split) % a.kv_heads;
   PagedTile w;
-  if (a.one_tile)
-    w.seq = t_block, w.tile = 0, w.tiles = 1;
-  else if (!find_tile(a, t_block, kRowsT, w))
-    return;
+  w.seq = t_block, w.tile = 0, w.tiles = 1;
   load_range(a, w);
-  const int r0 = w.tile * kRowsT, n_rows = min(w.lq, a.max_q) * a.group;
-  if (r0 >= n_rows) return;
-  const int here = min(n_rows - r0, kRowsT);  // rows of this tile
+  const int r0 = 0, n_rows = min(w.lq, a.max_q) * a.group;
+  if (n_rows == 0) return;
+  const int here = n_rows;  // at most 32
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int tok0 = r0 / a.group, tok1 = (r0 + here - 1) / a.group;
   const LaneRow x = lane_row(a, w, kv_head, r0 + (lane & 31), n_rows);
@@ -361,7 +393,7 @@ __global__ __launch_bounds__(64 * token_waves<D>(), 1) void paged_token_kernel(P
 
   int n_tiles, kbeg = 0, splits = 1, entries = 0;
   if (LISTED) {
-    entries = uniform(build_list<64 * NW>(a, w, kv_head, tok0, tok1 - tok0 + 1, split * a.chunk, a.chunk, s_list,
+    entries = uniform(build_list<64 * NW>(a, w, kv_head, r0, here, split, s_list,
                                           reinterpret_cast<uint32_t*>(&smem0[0][0][0])));
     n_tiles = ((entries << (a.s.shift - 4)) + 1) / 2;
     if (n_tiles == 0 && a.slots > 1) return empty(slot);
@@ -388,15 +420,7 @@ __global__ __launch_bounds__(64 * token_waves<D>(), 1) void paged_token_kernel(P
   }
   const uint32_t every = tok1 - tok0 == 31 ? ~0u : (2u << (tok1 - tok0)) - 1;
   auto find = [&](int t, int hh) -> Half {
-    if (!LISTED) return table_half(a, table, kbeg + kKeysT * t + 16 * hh);
-    const int i = 2 * t + hh, e = i >> (a.s.shift - 4);
-    const ListEntry entry = s_list[min(e, entries - 1)];
-    const int page = uniform(entry.page), block = uniform(entry.block);
-    Half y;
-    y.page = max(page, 0);
-    y.key = (block << a.s.shift) + 16 * (i & (slot_mask >> 4));
-    y.visible = e < entries ? uniform(static_cast<int>(entry.tokens)) : 0u;
-    return y;
+    return LISTED ? list_half(a, s_list, entries, 2 * t + hh, 0) : table_half(a, table, kbeg + kKeysT * t + 16 * hh);
   };
   struct Pair {
     Half h[2];
@@ -416,14 +440,15 @@ __global__ __launch_bounds__(64 * token_waves<D>(), 1) void paged_token_kernel(P
 
   RowState<D> st;
   st.clear();
-  Pair now, next;
+  Pair now, next, after;  // the tile in use, the one that is loaded, the one whose pages are looked up
   // Tile t is in one stage; the reads of the other have returned: refill it.
   auto turn = [&](uint8_t (&to)[2][kTile], int t) {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), other counters untouched
     if (t + NW < n_tiles) {
-      next = find_pair(t + NW);
+      next = after;
       issue(to, next);
+      after = find_pair(min(t + 2 * NW, n_tiles - 1));
       wait_vmcnt<4 * kHalfOps>();
     } else {
       wait_vmcnt<0>();
@@ -437,28 +462,45 @@ __global__ __launch_bounds__(64 * token_waves<D>(), 1) void paged_token_kernel(P
            (p.h[0].visible & p.h[1].visible & every) == every;
   };
   const int tk = static_cast<int>(x.q_row) - w.q0 - tok0;  // the lane's token
+  // Tiles that end behind some row's last key may hold anything there.  Where rows differ in
+  // the blocks that they list, what is hidden from one is some other's value, and all but
+  // always finite: these tiles are only looked through if an output says otherwise, in a second pass.
+  bool careful = false;
   auto masked = [&](const uint8_t (&from)[2][kTile], int t) {
+    const bool ends = now.h[0].key + 15 > lim_first || now.h[1].key + 15 > lim_first;
     Limits<1> lim;
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh)
       lim.at[hh] = (now.h[hh].visible >> tk) & 1 ? x.limit - now.h[hh].key + 16 * hh : -1;
-    attend_halves<D, 1>(from[0], from[1], q, st, a.c, lim, a.v.row_stride,
+    attend_halves<D, 1>(from[0], from[1], q, st, a.c, lim, KEYS != kListSeveral || careful || ends, a.v.row_stride,
                         [&](int i) { return half_base(a.v, find(t, i), slot_mask, kv_head); });
   };
   int t = wave;
-  if (t < n_tiles) {
-    now = find_pair(t);
-    issue(smem0[wave], now);
-  }
+  auto start = [&] {
+    if (t < n_tiles) {
+      now = find_pair(t);
+      issue(smem0[wave], now);
+      after = find_pair(min(t + NW, n_tiles - 1));
+    }
+  };
+  start();
   if (KEYS == kListSeveral) {
-    for (; t < n_tiles; t += 2 * NW) {
-      turn(smem1[wave], t);
-      masked(smem0[wave], t);
-      now = next;
-      if (t + NW >= n_tiles) break;
-      turn(smem0[wave], t + NW);
-      masked(smem1[wave], t + NW);
-      now = next;
+    for (;;) {
+      for (; t < n_tiles; t += 2 * NW) {
+        turn(smem1[wave], t);
+        masked(smem0[wave], t);
+        now = next;
+        if (t + NW >= n_tiles) break;
+        turn(smem0[wave], t + NW);
+        masked(smem1[wave], t + NW);
+        now = next;
+      }
+      if (careful || !not_finite(st)) break;
+      careful = true;
+      st.clear();
+      t = wave;
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // the reads of both stages have returned
+      start();
     }
   } else {
     // tiles that every row sees whole, in pairs; the rest
@@ -532,19 +574,28 @@ __global__ __launch_bounds__(64 * token_waves<D>(), 1) void paged_token_kernel(P
 constexpr int kRowsP = 128;  // rows of a block: 4 waves x 32
 constexpr int kKeysP = 64;   // keys of a tile
 
-template <int D, bool PREFIX>
+// Where the rows kernel's keys come from: the table (a sequence's own keys), the prefix
+// of a group, or listed blocks.
+enum RowKeys { kOwn, kPrefix, kListed };
+
+template <int D, RowKeys KEYS>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(PagedArgs a) {
+  constexpr bool PREFIX = KEYS == kPrefix, LISTED = KEYS == kListed;
   constexpr int kTile = kKeysP * 2 * D;
   constexpr int kOps = kTile / 4096;  // DMA instructions per wave and tile
   // two variables: see paged_token_kernel
   __shared__ __attribute__((aligned(1024))) uint8_t smem0[2][kTile];
   __shared__ __attribute__((aligned(1024))) uint8_t smem1[2][kTile];
+  __shared__ ListEntry<4> s_list[LISTED ? kList : 1];
+  static_assert(sizeof(smem0) >= 4 * (2 * kWords + 16), "the list's scratch is in a stage");
   const int kv_head = blockIdx.x % a.kv_heads, split = blockIdx.y;
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   PagedTile w;
   LaneRow x;
-  // the last key that some row of the wave sees; the last that every row of the block sees; keys of the block
-  int lim_last, block_first, all;
+  int r0 = 0, n_rows = 0;
+  // the last key that some row of the wave sees; the last that every row of the block sees; keys of the
+  // block; the last key that every row of the wave sees
+  int lim_last, block_first, all, lim_first = 0;
   if (PREFIX) {
     GroupRange g;
     if (!find_group_tile(a, blockIdx.x / a.kv_heads, kRowsP, w, g)) return;
@@ -574,26 +625,36 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(Paged
   } else {
     if (!find_tile(a, blockIdx.x / a.kv_heads, kRowsP, w)) return;
     load_range(a, w);
-    const int r0 = (w.tiles - 1 - w.tile) * kRowsP;  // the last tiles see the most keys: first
-    const int n_rows = min(w.lq, a.max_q) * a.group, rw = r0 + 32 * wave;
+    r0 = (w.tiles - 1 - w.tile) * kRowsP;  // the last tiles see the most keys: first
+    n_rows = min(w.lq, a.max_q) * a.group;
+    const int rw = r0 + 32 * wave;
     x = lane_row(a, w, kv_head, rw + (lane & 31), n_rows);
     block_first = last_key(w, r0 / a.group);
+    lim_first = last_key(w, min(rw, n_rows - 1) / a.group);
     lim_last = last_key(w, min(rw + 31, n_rows - 1) / a.group);
     all = max(last_key(w, (min(r0 + kRowsP, n_rows) - 1) / a.group) + 1 - w.own, 0);
   }
   const int chunk = PREFIX ? a.prefix_chunk : a.chunk;
   const int slot = PREFIX ? split : a.prefix_splits + split;
-  const int splits = (all + chunk - 1) / chunk;  // that have keys to see
   auto empty = [&](int at) {
     if (x.valid && lane < 32) empty_share(a, at, x.q_row, x.head);
   };
-  if (!PREFIX && a.n_groups > 0 && split == 0 && w.own == 0)
-    for (int i = 0; i < a.prefix_splits; ++i) empty(i);
-  if (split >= max(splits, a.n_groups > 0 ? 0 : 1)) {
-    if (a.n_groups > 0) empty(slot);
-    return;
+  int splits = 1, entries = 0, kbeg = 0, kend;  // listed: kbeg and kend count the list's keys
+  if (LISTED) {
+    entries = uniform(build_list<256>(a, w, kv_head, r0, min(n_rows - r0, kRowsP), split, s_list,
+                                      reinterpret_cast<uint32_t*>(&smem0[0][0])));
+    kend = entries << a.s.shift;
+    if (kend == 0 && a.slots > 1) return empty(slot);
+  } else {
+    splits = (all + chunk - 1) / chunk;  // that have keys to see
+    if (!PREFIX && a.n_groups > 0 && split == 0 && w.own == 0)
+      for (int i = 0; i < a.prefix_splits; ++i) empty(i);
+    if (split >= max(splits, a.n_groups > 0 ? 0 : 1)) {
+      if (a.n_groups > 0) empty(slot);
+      return;
+    }
+    kbeg = w.own + split * chunk, kend = kbeg + min(all - split * chunk, chunk);
   }
-  const int kbeg = w.own + split * chunk, kend = kbeg + min(all - split * chunk, chunk);
 
   bf16x8 q[D / 16];
   load_q<D>(a, x, q);
@@ -612,10 +673,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(Paged
   struct Quad {
     Half h[4];
   };
-  auto find_quad = [&](int key) {
-    return Quad{{table_half(a, table, key), table_half(a, table, key + 16), table_half(a, table, key + 32),
-                 table_half(a, table, key + 48)}};
+  auto find = [&](int key) -> Half {
+    return LISTED ? list_half(a, s_list, entries, key >> 4, wave) : table_half(a, table, key);
   };
+  auto find_quad = [&](int key) { return Quad{{find(key), find(key + 16), find(key + 32), find(key + 48)}}; };
   auto issue = [&](uint8_t (&to)[2][kTile], const Quad& p) {
 #pragma unroll
     for (int i = 0; i < kOps; ++i) {
@@ -631,59 +692,99 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(Paged
 
   RowState<D> st;
   st.clear();
-  Quad now, next;
+  Quad now, next, after;  // the tile in use, the one that is loaded, the one whose pages are looked up
   // Tile `key` has arrived in one stage and every wave is done with the other: refill that.
   auto turn = [&](uint8_t (&to)[2][kTile], int key) {
     wait_vmcnt<0>();
     stage_barrier();
     if (key + kKeysP < kend) {
-      next = find_quad(key + kKeysP);
+      next = after;
       issue(to, next);
+      after = find_quad(min(key + 2 * kKeysP, kend - 1 & ~(kKeysP - 1)));
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto valid = [&](const Quad& p) {
-    return (p.h[0].visible & p.h[1].visible & p.h[2].visible & p.h[3].visible) != 0;
+  auto masked = [&](const uint8_t (&from)[2][kTile], int key, const Limits<kKeysP / 32>& lim, bool scan) {
+    attend_halves<D, kKeysP / 32>(from[0], from[1], q, st, a.c, lim, scan, a.v.row_stride,
+                                  [&](int i) { return half_base(a.v, find(key + 16 * i), slot_mask, kv_head); });
   };
-  int key = kbeg, stage = 0;
-  if (key < kend) {
-    now = find_quad(key);
-    issue(smem0, now);
-  }
-  // tiles that every row of the block sees whole, in pairs
-  const int full = min(kend, block_first + 1);
-  while (key + kKeysP <= full && valid(now)) {
-    turn(smem1, key);
-    attend<D, kKeysP / 32, false>(smem0[0], smem0[1], q, st, a.c, 0, false);
-    now = next;
-    key += kKeysP;
-    stage = 1;
-    if (key + kKeysP > full || !valid(now)) break;
-    turn(smem0, key);
-    attend<D, kKeysP / 32, false>(smem1[0], smem1[1], q, st, a.c, 0, false);
-    now = next;
-    key += kKeysP;
-    stage = 0;
-  }
-  // the rest
-  for (; key < kend; key += kKeysP, stage ^= 1) {
-    uint8_t(&from)[2][kTile] = stage ? smem1 : smem0;
-    turn(stage ? smem0 : smem1, key);
-    if (key <= lim_last) {
-      Limits<kKeysP / 32> lim;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) lim.at[i] = now.h[i].visible ? x.limit - key : -1;
-      attend_halves<D, kKeysP / 32>(from[0], from[1], q, st, a.c, lim, a.v.row_stride, [&](int i) {
-        return half_base(a.v, table_half(a, table, key + 16 * i), slot_mask, kv_head);
-      });
+  int key = kbeg;
+  auto start = [&] {
+    if (key < kend) {
+      now = find_quad(key);
+      issue(smem0, now);
+      after = find_quad(key + kKeysP);
     }
-    now = next;
+  };
+  start();
+  if (LISTED) {
+    const int tk = static_cast<int>(x.q_row) - w.q0 - (r0 + 32 * wave) / a.group;  // the lane's token of the wave's
+    bool careful = false;  // see paged_token_kernel
+    auto use = [&](const uint8_t (&from)[2][kTile], int key) {
+      if ((now.h[0].visible | now.h[1].visible | now.h[2].visible | now.h[3].visible) != 0) {
+        Limits<kKeysP / 32> lim;
+        int last = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          lim.at[i] = now.h[i].visible >> tk & 1 ? x.limit - now.h[i].key + 16 * i : -1;
+          last = max(last, now.h[i].key + 15);
+        }
+        masked(from, key, lim, careful || last > lim_first);
+      }
+      now = next;
+    };
+    for (;;) {
+      for (; key < kend; key += 2 * kKeysP) {
+        turn(smem1, key);
+        use(smem0, key);
+        if (key + kKeysP >= kend) break;
+        turn(smem0, key + kKeysP);
+        use(smem1, key + kKeysP);
+      }
+      if (careful || !__syncthreads_or(not_finite(st))) break;
+      careful = true;
+      st.clear();
+      key = kbeg;
+      start();
+    }
+  } else {
+    auto valid = [&](const Quad& p) {
+      return (p.h[0].visible & p.h[1].visible & p.h[2].visible & p.h[3].visible) != 0;
+    };
+    int stage = 0;
+    // tiles that every row of the block sees whole, in pairs
+    const int full = min(kend, block_first + 1);
+    while (key + kKeysP <= full && valid(now)) {
+      turn(smem1, key);
+      attend<D, kKeysP / 32, false>(smem0[0], smem0[1], q, st, a.c, 0, false);
+      now = next;
+      key += kKeysP;
+      stage = 1;
+      if (key + kKeysP > full || !valid(now)) break;
+      turn(smem0, key);
+      attend<D, kKeysP / 32, false>(smem1[0], smem1[1], q, st, a.c, 0, false);
+      now = next;
+      key += kKeysP;
+      stage = 0;
+    }
+    // the rest
+    for (; key < kend; key += kKeysP, stage ^= 1) {
+      uint8_t(&from)[2][kTile] = stage ? smem1 : smem0;
+      turn(stage ? smem0 : smem1, key);
+      if (key <= lim_last) {
+        Limits<kKeysP / 32> lim;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lim.at[i] = now.h[i].visible ? x.limit - key : -1;
+        masked(from, key, lim, true);
+      }
+      now = next;
+    }
   }
 
   const float l = sum_halves(st.l);
   if (!x.valid) return;
   const int h = lane >> 5;
-  const bool direct = a.n_groups == 0 && splits <= 1;
+  const bool direct = a.every_slot() ? a.slots == 1 : splits <= 1;
   const int64_t row = part_row(a, slot, x.q_row, x.head);
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
@@ -716,7 +817,7 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a) {
   int64_t q_row = u / a.q_heads;
   const int head = static_cast<int>(u - q_row * a.q_heads);
   int seq, pos;
-  if (a.one_tile) {  // u counts the rows below max_q of each sequence
+  if (a.token) {  // u counts the rows below max_q of each sequence
     seq = static_cast<int>(q_row / a.max_q);
     if (seq >= a.s.n_seqs) return;
     pos = static_cast<int>(q_row - static_cast<int64_t>(seq) * a.max_q);
@@ -731,7 +832,7 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a) {
     pos = 0;
   }
   const PagedRange w = sequence(a, seq, 0);
-  if (a.one_tile)
+  if (a.token)
     q_row = w.q0 + pos;
   else
     pos = static_cast<int>(q_row) - w.q0;
@@ -802,16 +903,17 @@ constexpr int kRounds = 64;
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Plan {
-  bool token, one_tile;
+  bool token;                   // the few-rows kernel: every sequence is one tile
   int64_t tiles, prefix_tiles;  // row tiles x key heads
-  int chunk, splits;            // of the own keys (listed blocks)
+  int chunk, splits;            // own keys of a split (listed blocks: the fewest); splits
   int prefix_chunk, prefix_splits;
   int slots() const { return splits + prefix_splits; }
 };
 
-// Tokens that a tile of the token kernel may hold rows of.
-int tile_tokens(int group, int max_q) {
-  const int n = kRowsT % group == 0 ? kRowsT / group : group % kRowsT == 0 ? 1 : (kRowsT - 2) / group + 2;
+// Tokens that a tile may hold rows of.
+int tile_tokens(int group, int max_q, bool token) {
+  const int rows = token ? kRowsT : kRowsP;
+  const int n = rows % group == 0 ? rows / group : group % rows == 0 ? 1 : (rows - 2) / group + 2;
   return std::min(n, max_q);
 }
 
@@ -829,25 +931,28 @@ Plan make_plan(const moe_paged_attn& d) {
   const int64_t g = s.q_heads / s.kv_heads;
   const int64_t seqs = std::min<int64_t>(s.n_seqs, s.q_rows);
   const bool listed = d.n_blocks > 0, grouped = d.n_groups > 0;
-  p.one_tile = d.max_q * g <= kRowsT;
-  p.token = p.one_tile || listed;
-  p.tiles = (p.one_tile ? s.n_seqs : seqs + s.q_rows * g / (p.token ? kRowsT : kRowsP)) * s.kv_heads;
+  p.token = d.max_q * g <= kRowsT;
+  p.tiles = (p.token ? s.n_seqs : seqs + s.q_rows * g / kRowsP) * s.kv_heads;
   const int64_t tiles = std::max<int64_t>(p.tiles, 1);
   int64_t keys = std::max(d.max_kv, 1);
   if (grouped) keys += s.page_size - 1;  // what is left of the prefix's last page
   if (listed)
-    keys = std::max<int64_t>(1, std::min<int64_t>(static_cast<int64_t>(tile_tokens(g, d.max_q)) * d.n_blocks,
+    keys = std::max<int64_t>(1, std::min<int64_t>(static_cast<int64_t>(tile_tokens(g, d.max_q, p.token)) * d.n_blocks,
                                                   ceil_div(keys, s.page_size))) * s.page_size;
   const int64_t unit = p.token ? kKeysT * (s.head_dim == 256 ? 2 : 4) : kKeysP;
   const int64_t want = s.head_dim > (p.token ? 64 : 128) ? kCus : 2 * kCus;
   const int64_t least = p.token ? (keys <= 4 * unit ? 4 : 2) * unit
                                 : std::min(std::max(tiles / 16, int64_t{4}), int64_t{16}) * unit;
-  const int64_t most = !p.token ? INT32_MAX
+  const int64_t most = !p.token || listed ? INT32_MAX
                                 : std::max(16 * unit, ceil_div(keys, std::max(kRounds * kCus / tiles, int64_t{1})));
   const int64_t chunk = pick_chunk(keys, p.tiles, unit, want, least, most);
   if (listed) {
-    p.chunk = static_cast<int>(std::min<int64_t>(ceil_div(chunk, s.page_size), kList));
-    p.splits = static_cast<int>(ceil_div(keys / s.page_size, p.chunk));
+    // How many blocks a tile's tokens list together is known to the kernel alone: as many as one
+    // of them at least, and hardly more where they agree.
+    const int64_t least_blocks = std::max<int64_t>(least / s.page_size, 1);
+    const int64_t wanted = std::min(ceil_div(want, tiles), ceil_div(std::min<int64_t>(d.n_blocks, keys / s.page_size), least_blocks));
+    p.chunk = static_cast<int>(least_blocks);
+    p.splits = static_cast<int>(std::max(wanted, ceil_div(keys / s.page_size, kList)));
   } else {
     p.chunk = static_cast<int>(std::min<int64_t>(chunk, 1 << 30));
     p.splits = static_cast<int>(ceil_div(keys, chunk));
@@ -891,19 +996,21 @@ int check_shape(const moe_paged_attn* a) {
 template <int D>
 void launch(const PagedArgs& a, const Plan& p, hipStream_t s) {
   if (p.prefix_splits)
-    paged_rows_kernel<D, true><<<dim3(static_cast<unsigned>(p.prefix_tiles), static_cast<unsigned>(p.prefix_splits)),
+    paged_rows_kernel<D, kPrefix><<<dim3(static_cast<unsigned>(p.prefix_tiles), static_cast<unsigned>(p.prefix_splits)),
                                  256, 0, s>>>(a);
   const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>(p.splits));
-  if (a.n_blocks && tile_tokens(a.group, a.max_q) == 1)
-    paged_token_kernel<D, kListOne><<<grid, 64 * token_waves<D>(), 0, s>>>(a);
-  else if (a.n_blocks)
-    paged_token_kernel<D, kListSeveral><<<grid, 64 * token_waves<D>(), 0, s>>>(a);
-  else if (p.token)
+  if (!p.token && a.n_blocks)
+    paged_rows_kernel<D, kListed><<<grid, 256, 0, s>>>(a);
+  else if (!p.token)
+    paged_rows_kernel<D, kOwn><<<grid, 256, 0, s>>>(a);
+  else if (!a.n_blocks)
     paged_token_kernel<D, kTable><<<grid, 64 * token_waves<D>(), 0, s>>>(a);
+  else if (a.max_q == 1)
+    paged_token_kernel<D, kListOne><<<grid, 64 * token_waves<D>(), 0, s>>>(a);
   else
-    paged_rows_kernel<D, false><<<grid, 256, 0, s>>>(a);
+    paged_token_kernel<D, kListSeveral><<<grid, 64 * token_waves<D>(), 0, s>>>(a);
   if (a.slots > 1) {
-    const int64_t rows = (a.one_tile ? static_cast<int64_t>(a.s.n_seqs) * a.max_q : a.s.q_rows) * a.q_heads;
+    const int64_t rows = (a.token ? static_cast<int64_t>(a.s.n_seqs) * a.max_q : a.s.q_rows) * a.q_heads;
     paged_join_kernel<D><<<static_cast<unsigned>(ceil_div(rows, a.join_rows)), 256, 0, s>>>(a);
   }
 }
@@ -950,9 +1057,9 @@ int moe_paged_attention(const moe_paged_attn* a, void* ws, size_t ws_bytes, void
   k.q_heads = p.q_heads, k.kv_heads = p.kv_heads, k.group = p.q_heads / p.kv_heads;
   k.max_q = a->max_q, k.n_groups = a->n_groups, k.n_blocks = a->n_blocks;
   k.max_kv = std::min(a->max_kv, k.s.capacity), k.max_prefix = std::min(a->max_prefix, k.s.capacity);
-  k.chunk = plan.chunk, k.prefix_chunk = plan.prefix_chunk, k.prefix_splits = plan.prefix_splits;
+  k.chunk = plan.chunk, k.splits = plan.splits, k.prefix_chunk = plan.prefix_chunk, k.prefix_splits = plan.prefix_splits;
   k.slots = plan.slots();
-  k.one_tile = plan.one_tile, k.token = plan.token;
+  k.token = plan.token;
   k.tile_rows = plan.token ? moe::kRowsT : moe::kRowsP;
   k.join_rows = plan.slots() > moe::kJoinShared ? 1 : 256 / (p.head_dim / 4);
   k.scale = a->scale;
