@@ -257,36 +257,55 @@ struct ListEntry {
 };
 
 // Marks are set with integer atomics (their order changes nothing) in LDS, one bit a
-// block; a block's place in the list is the number of marks below it.  scratch: at
-// least 2 * kWords + 16 ints; r0: the tile's first row, rows: its rows.  Returns the number of
-// entries of this split's share (at most kList: the plan sees to it).
+// block; a block's place in the list is the number of marks below it.  A thread keeps its
+// first kHeld ids and their pages in registers, so a list costs three loads in a row.
+// scratch: at least 2 * kWords + 16 ints; r0: the tile's first row, rows: its rows.  Returns
+// the number of entries of this split's share (at most kList: the plan sees to it).
 template <int THREADS, int PARTS>
 __device__ int build_list(const PagedArgs& a, const PagedTile& w, int kv_head, int r0, int rows, int split,
                           ListEntry<PARTS>* list, uint32_t* scratch) {
+  constexpr int kPer = kWords / THREADS, kHeld = 4;
   const int tid = threadIdx.x;
   uint32_t* marks = scratch;
   int* below = reinterpret_cast<int*>(scratch + kWords);
   int* wave_sum = reinterpret_cast<int*>(scratch + 2 * kWords);
   const int tok0 = r0 / a.group, n_tok = (r0 + rows - 1) / a.group - tok0 + 1;
-  const int n = (max(last_key(w, tok0 + n_tok - 1), -1) >> a.s.shift) + 1;  // blocks there are to see
-  const int words = min((n + 31) / 32, kWords);
-  for (int i = tid; i < words; i += THREADS) marks[i] = 0;
-  __syncthreads();
   const int total = n_tok * a.n_blocks;
   const int32_t* ids = a.blocks + (static_cast<int64_t>(w.q0 + tok0) * a.kv_heads + kv_head) * a.n_blocks;
   const int64_t to_next = static_cast<int64_t>(a.kv_heads) * a.n_blocks;
-  for (int i = tid; i < total; i += THREADS) {
+  const int32_t* table = a.s.table + w.seq * a.s.table_stride;
+  // id i of the tile: a block that its token sees a key of, or -1
+  auto load_id = [&](int i) {
+    if (i >= total) return -1;
     const int t = i / a.n_blocks;
     const int id = ids[t * to_next + i - t * a.n_blocks];
-    if (id >= 0 && id < 32 * words && (id << a.s.shift) <= last_key(w, tok0 + t)) atomicOr(&marks[id >> 5], 1u << (id & 31));
+    return id >= 0 && id < 32 * kWords && id << a.s.shift <= last_key(w, tok0 + t) ? id : -1;
+  };
+  int id[kHeld], page[kHeld];
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) id[j] = load_id(tid + j * THREADS);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) marks[tid + i * THREADS] = 0;
+  for (int i = tid; i < kList; i += THREADS) {
+    list[i].page = -1;
+#pragma unroll
+    for (int j = 0; j < PARTS; ++j) list[i].tokens[j] = 0;
   }
   __syncthreads();
-  constexpr int kPer = kWords / THREADS;
+  auto mark = [&](int i) {
+    if (i >= 0) atomicOr(&marks[i >> 5], 1u << (i & 31));
+  };
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+    mark(id[j]);
+    page[j] = id[j] >= 0 ? table[id[j]] : -1;
+  }
+  for (int i = tid + kHeld * THREADS; i < total; i += THREADS) mark(load_id(i));
+  __syncthreads();
   int mine[kPer], local = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int at = tid * kPer + i;
-    mine[i] = at < words ? __popc(marks[at]) : 0;
+    mine[i] = __popc(marks[tid * kPer + i]);
     local += mine[i];
   }
   const int incl = wave_incl_scan(local);
@@ -298,43 +317,34 @@ __device__ int build_list(const PagedArgs& a, const PagedTile& w, int kv_head, i
     if (i < (tid >> 6)) run += wave_sum[i];
     all += wave_sum[i];
   }
-  const int count = min(max((all + a.splits - 1) / a.splits, a.chunk), kList), lo = split * count;
-  const int32_t* table = a.s.table + w.seq * a.s.table_stride;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int at = tid * kPer + i;
-    if (at < words) below[at] = run;
-    if (mine[i] && run < lo + count && run + mine[i] > lo) {
-      uint32_t m = marks[at];
-      for (int r = run; m; ++r, m &= m - 1) {
-        if (r < lo || r >= lo + count) continue;
-        const int block = 32 * at + __ffs(m) - 1;
-        const int p = table[min(block, a.s.table_pages - 1)];
-        const bool ok = p >= 0 && p < a.s.n_pages;
-        list[r - lo].page = ok ? p : -1;
-        list[r - lo].block = block;
-#pragma unroll
-        for (int j = 0; j < PARTS; ++j) list[r - lo].tokens[j] = n_tok == 1 && ok ? 1u : 0u;
-      }
-    }
+    below[tid * kPer + i] = run;
     run += mine[i];
   }
   __syncthreads();
-  if (n_tok > 1) {
-    for (int i = tid; i < total; i += THREADS) {
-      const int t = i / a.n_blocks;
-      const int id = ids[t * to_next + i - t * a.n_blocks];
-      if (id < 0 || id >= 32 * words || (id << a.s.shift) > last_key(w, tok0 + t)) continue;
-      const int r = below[id >> 5] + __popc(marks[id >> 5] & ((1u << (id & 31)) - 1)) - lo;
-      if (r < 0 || r >= count || list[r].page < 0) continue;
+  const int count = min(max((all + a.splits - 1) / a.splits, a.chunk), kList), lo = split * count;
+  auto enter = [&](int i, int block, int p) {
+    if (block < 0) return;
+    const int r = below[block >> 5] + __popc(marks[block >> 5] & ((1u << (block & 31)) - 1)) - lo;
+    if (r < 0 || r >= count) return;
+    list[r].block = block;  // threads that hold the same block write the same
+    if (p < 0 || p >= a.s.n_pages) return;
+    list[r].page = p;
+    const int t = i / a.n_blocks;
 #pragma unroll
-      for (int j = 0; j < PARTS; ++j) {
-        const int from = (r0 + 32 * j) / a.group - tok0, to = (r0 + 32 * j + 31) / a.group - tok0;
-        if (t >= from && t <= to) atomicOr(&list[r].tokens[j], 1u << (t - from));
-      }
+    for (int j = 0; j < PARTS; ++j) {
+      const int from = (r0 + 32 * j) / a.group - tok0, to = (r0 + 32 * j + 31) / a.group - tok0;
+      if (t >= from && t <= to) atomicOr(&list[r].tokens[j], 1u << (t - from));
     }
-    __syncthreads();
+  };
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) enter(tid + j * THREADS, id[j], page[j]);
+  for (int i = tid + kHeld * THREADS; i < total; i += THREADS) {
+    const int block = load_id(i);
+    enter(i, block, block >= 0 ? table[block] : -1);
   }
+  __syncthreads();
   return min(max(all - lo, 0), count);
 }
 
