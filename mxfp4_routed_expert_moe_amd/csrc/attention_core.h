@@ -108,10 +108,14 @@ __device__ __forceinline__ int limit_of(const Limits<NT>& lim, int i) { return l
 // Attend to NT x 32 keys: ks and vs are the tile's rows in LDS, c = scale *
 // log2(e), lim the last visible key of the lane's row, counted in the tile.
 // dirty: values that are not finite count as zeros (masked tiles only).
-template <int D, int NT, bool MASKED, typename Lim>
+// KEEP = false: the LDS addresses are not kept in registers from tile to tile (a lane number that the
+// compiler takes for new has none), which a kernel does where it has no registers left.
+template <int D, int NT, bool MASKED, bool KEEP = true, typename Lim>
 __device__ __forceinline__ void attend(const uint8_t* ks, const uint8_t* vs, const bf16x8 (&q)[D / 16],
                                        RowState<D>& st, float c, Lim lim, bool dirty) {
-  const int lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
+  int lane = threadIdx.x & 63;
+  if constexpr (!KEEP) asm volatile("" : "+v"(lane));
+  const int n = lane & 31, h = lane >> 5;
   f32x16 s[NT];
   u32x4 kf[2][NT];  // the next step's operands are read while this one's are used
   auto read_k = [&](int i) {

@@ -188,12 +188,12 @@ __device__ bool find_run(const PagedSeqs& s, int u, Run& r) {
       lq = min(x.lq - skip, max(s.capacity - first, 0));
       runs = lq > 0 ? ((first + lq - 1) >> s.shift) - (first >> s.shift) + 1 : 0;
     }
-    const int incl = wave_incl_scan(runs);
+    const int incl = wave_prefix(runs);
     const uint64_t past = __ballot(incl > u);
     if (past) {
       const int src = __ffsll(static_cast<unsigned long long>(past)) - 1;
-      q0 = __shfl(q0, src, 64), lq = __shfl(lq, src, 64), first = __shfl(first, src, 64);
-      const int i = u - (__shfl(incl, src, 64) - __shfl(runs, src, 64));
+      q0 = lane_value(q0, src), lq = lane_value(lq, src), first = lane_value(first, src);
+      const int i = u - (lane_value(incl, src) - lane_value(runs, src));
       // run i: positions of the sequence's i-th page
       const int begin = i == 0 ? first : ((first >> s.shift) + i) << s.shift;
       const int end = min(first + lq, ((first >> s.shift) + i + 1) << s.shift);
@@ -203,7 +203,7 @@ __device__ bool find_run(const PagedSeqs& s, int u, Run& r) {
       r.pos0 = __builtin_amdgcn_readfirstlane(begin);
       return true;
     }
-    u -= __shfl(incl, 63, 64);
+    u -= lane_value(incl, 63);
   }
   return false;
 }

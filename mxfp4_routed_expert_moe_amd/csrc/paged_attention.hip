@@ -37,6 +37,7 @@ struct PagedArgs {
   int chunk, splits; // own keys of a split (listed blocks: the fewest), and how many there are at most
   int prefix_chunk;  // prefix keys of a split
   int prefix_splits, slots;
+  int tiles, prefix_tiles, units, prefix_units;  // of the rows kernel: row tiles, and (tile, split) pairs
   int token;         // the token kernel did the own keys: every sequence is one tile of it
   int tile_rows;     // rows of a tile of the kernel that did the own keys
   int join_rows;     // rows of a block of the join
@@ -45,17 +46,18 @@ struct PagedArgs {
 };
 
 // ---------------------------------------------------------------- work
-// The prefix length that sequence b's group names (0 without one).  The last group
-// that begins at or before b.
-__device__ __forceinline__ int prefix_of(const PagedArgs& a, int b) {
-  if (a.n_groups == 0) return 0;
-  int lo = 0, hi = a.n_groups;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.cu_group[mid] <= b) lo = mid; else hi = mid;
+// The prefix length that sequence b's group names (0 without one): the last group that
+// begins at or before b.  For a whole wave, 64 groups at a time.
+__device__ int prefix_of(const PagedArgs& a, int b) {
+  const int lane = threadIdx.x & 63;
+  for (int base = 0; base < a.n_groups; base += 64) {
+    const int g = min(base + lane, a.n_groups - 1);
+    const GroupRange r = group_range(a.cu_group, g, a.s.n_seqs);
+    const int len = a.prefix_len[g];
+    const uint64_t mine = __ballot(b >= r.first && b < r.past);
+    if (mine) return lane_value(len, 63 - __clzll(static_cast<long long>(mine)));
   }
-  const GroupRange g = group_range(a.cu_group, lo, a.s.n_seqs);
-  return b >= g.first && b < g.past ? a.prefix_len[lo] : 0;
+  return 0;
 }
 
 __device__ __forceinline__ PagedRange sequence(const PagedArgs& a, int b, int prefix) {
@@ -71,23 +73,26 @@ struct PagedTile : PagedRange {
 __device__ bool find_tile(const PagedArgs& a, int t, int rows, PagedTile& w) {
   const int lane = threadIdx.x & 63;
   for (int base = 0; base < a.s.n_seqs; base += 64) {
-    int nt = 0;
-    if (base + lane < a.s.n_seqs)
-      nt = (min(sequence(a, base + lane, 0).lq, a.max_q) * a.group + rows - 1) / rows;
-    const int incl = wave_incl_scan(nt);
+    const bool there = base + lane < a.s.n_seqs;
+    const PagedRange r = sequence(a, there ? base + lane : base, 0);
+    const int nt = there ? (min(r.lq, a.max_q) * a.group + rows - 1) / rows : 0;
+    const int incl = wave_prefix(nt);
     const uint64_t past = __ballot(incl > t);
     if (past) {
       const int src = __ffsll(static_cast<unsigned long long>(past)) - 1;
-      w.seq = uniform(base + src);
-      w.tiles = uniform(__shfl(nt, src, 64));
-      w.tile = uniform(t - (__shfl(incl, src, 64) - w.tiles));
+      w.seq = base + src;
+      w.q0 = lane_value(r.q0, src), w.lq = lane_value(r.lq, src), w.diag = lane_value(r.diag, src);
+      w.own = lane_value(r.own, src), w.end = lane_value(r.end, src);
+      w.tiles = lane_value(nt, src);
+      w.tile = t - (lane_value(incl, src) - w.tiles);
       return true;
     }
-    t -= uniform(__shfl(incl, 63, 64));
+    t -= lane_value(incl, 63);
   }
   return false;
 }
 
+// The range of a sequence behind its group's prefix.
 __device__ __forceinline__ void load_range(const PagedArgs& a, PagedTile& w) {
   const PagedRange r = sequence(a, w.seq, prefix_of(a, w.seq));
   w.q0 = uniform(r.q0), w.lq = uniform(r.lq), w.diag = uniform(r.diag);
@@ -108,23 +113,19 @@ __device__ bool find_group_tile(const PagedArgs& a, int t, int rows, PagedTile& 
       lq = min(max(a.s.cu_q[x.past], q0), a.s.q_rows) - q0;
       nt = keys > 0 ? (lq * a.group + rows - 1) / rows : 0;
     }
-    const int incl = wave_incl_scan(nt);
+    const int incl = wave_prefix(nt);
     const uint64_t past = __ballot(incl > t);
     if (past) {
       const int src = __ffsll(static_cast<unsigned long long>(past)) - 1;
-      g.first = uniform(__shfl(x.first, src, 64));
-      g.past = uniform(__shfl(x.past, src, 64));
+      g.first = lane_value(x.first, src), g.past = lane_value(x.past, src);
       w.seq = g.first;
-      w.q0 = uniform(__shfl(q0, src, 64));
-      w.lq = uniform(__shfl(lq, src, 64));
-      w.own = 0;
-      w.end = uniform(__shfl(keys, src, 64));
-      w.diag = 0;
-      w.tiles = uniform(__shfl(nt, src, 64));
-      w.tile = uniform(t - (__shfl(incl, src, 64) - w.tiles));
+      w.q0 = lane_value(q0, src), w.lq = lane_value(lq, src);
+      w.own = 0, w.end = lane_value(keys, src), w.diag = 0;
+      w.tiles = lane_value(nt, src);
+      w.tile = t - (lane_value(incl, src) - w.tiles);
       return true;
     }
-    t -= uniform(__shfl(incl, 63, 64));
+    t -= lane_value(incl, 63);
   }
   return false;
 }
@@ -175,6 +176,10 @@ __device__ __forceinline__ void empty_share(const PagedArgs& a, int slot, int64_
   a.part_ml[part_row(a, slot, q_row, head)] = make_float2(kNegInf, 0.f);
 }
 
+// Heads of 256 leave no registers for the addresses.
+template <int D>
+constexpr bool kKeep = D < 256;
+
 // A tile whose rows see some of its 16-key halves only, or none: as attend_masked of the
 // contiguous kernels, with a limit per half; row(i): the values of half i's first key.
 // scan = false: every value of the tile is taken for finite.
@@ -183,7 +188,7 @@ __device__ __forceinline__ void attend_halves(const uint8_t* ks, const uint8_t* 
                                               RowState<D>& st, float c, const Limits<NT>& lim, bool scan,
                                               int64_t row_stride, Row row) {
   const bool dirty = scan && any_not_finite(vs, NT * 32 * 2 * D);
-  attend<D, NT, true>(ks, vs, q, st, c, lim, dirty);
+  attend<D, NT, true, kKeep<D>>(ks, vs, q, st, c, lim, dirty);
   if (!dirty) return;
   const int h = (threadIdx.x & 63) >> 5;
   for (int r = 0; r < NT * 32; ++r) {
@@ -217,25 +222,60 @@ __device__ __forceinline__ bool not_finite(const RowState<D>& st) {
   return __any(zero != 0.f);
 }
 
-// Sixteen keys: where they are, and the position of the first.
-struct Half {
-  int page, key;     // a page that there is
-  uint32_t visible;  // of the tile's tokens: bit (token - the tile's first); 0 where the page is none
+// Neighbouring keys of one page: 16, or a tile where a page holds whole tiles.
+struct Spot {
+  int page, key;     // a page that there is, the position of the first key
+  uint32_t visible;  // of the rows' tokens: bit (token - the first); 0 where the page is none
+};
+// A tile's N spots.
+template <int N>
+struct Spots {
+  Spot at[N];
 };
 
-__device__ __forceinline__ const uint16_t* half_base(const moe_pages& p, const Half& x, int slot_mask, int kv_head) {
+__device__ __forceinline__ const uint16_t* spot_base(const moe_pages& p, const Spot& x, int slot_mask, int kv_head) {
   return p.base + x.page * p.page_stride + (x.key & slot_mask) * p.row_stride + kv_head * p.head_stride;
 }
 
-// The half at key `key` of the table row, for every token.
-__device__ __forceinline__ Half table_half(const PagedArgs& a, ConstInts table, int key) {
-  Half x;
-  const int p = table[min(key >> a.s.shift, a.s.table_pages - 1)];
-  const bool ok = p >= 0 && p < a.s.n_pages;
-  x.page = ok ? p : 0;
-  x.key = key;
-  x.visible = ok ? ~0u : 0u;
-  return x;
+// What a lookup brings: used one tile later, so that nothing waits for it.
+struct Found {
+  int page, key;
+  uint32_t tokens;
+};
+template <int N>
+struct FoundAll {
+  Found at[N];
+};
+
+// The spot at key `key` of the table row, for every token.
+__device__ __forceinline__ Found look_up(const PagedArgs& a, ConstInts table, int key) {
+  return Found{table[min(key >> a.s.shift, a.s.table_pages - 1)], key, ~0u};
+}
+__device__ __forceinline__ Spot to_spot(const PagedArgs& a, Found f) {
+  const int page = uniform(f.page);
+  const bool ok = page >= 0 && page < a.s.n_pages;
+  return Spot{ok ? page : 0, uniform(f.key), ok ? static_cast<uint32_t>(uniform(static_cast<int>(f.tokens))) : 0u};
+}
+template <int N>
+__device__ __forceinline__ Spots<N> to_spots(const PagedArgs& a, const FoundAll<N>& f) {
+  Spots<N> p;
+#pragma unroll
+  for (int i = 0; i < N; ++i) p.at[i] = to_spot(a, f.at[i]);
+  return p;
+}
+
+// Last keys that a row sees in the tile's halves, given the last that it sees at all and
+// its token.
+template <int NT, int N>
+__device__ __forceinline__ Limits<NT> spot_limits(const Spots<N>& p, int limit, int token) {
+  constexpr int kEach = 2 * NT / N;  // halves of a spot
+  Limits<NT> lim;
+#pragma unroll
+  for (int i = 0; i < 2 * NT; ++i) {
+    const Spot& x = p.at[i / kEach];
+    lim.at[i] = x.visible >> token & 1 ? limit - x.key + 16 * (i / kEach * kEach) : -1;
+  }
+  return lim;
 }
 
 // ---------------------------------------------------------------- few rows
@@ -243,8 +283,6 @@ constexpr int kRowsT = 32;  // rows of a tile
 constexpr int kKeysT = 32;  // keys of a wave's tile
 constexpr int kList = 512;  // listed blocks of a split
 constexpr int kWords = 1024;  // 32-block words of the marks: blocks per sequence / 32
-template <int D>
-constexpr int token_waves() { return D == 256 ? 2 : 4; }
 
 // The listed blocks of a tile's tokens, each once and ascending, of which the splits
 // take equal shares (as many as `least` there are, or less in the last).  An entry is a
@@ -308,7 +346,7 @@ __device__ int build_list(const PagedArgs& a, const PagedTile& w, int kv_head, i
     mine[i] = __popc(marks[tid * kPer + i]);
     local += mine[i];
   }
-  const int incl = wave_incl_scan(local);
+  const int incl = wave_prefix(local);
   if ((tid & 63) == 63) wave_sum[tid >> 6] = incl;
   __syncthreads();
   int run = incl - local, all = 0;
@@ -348,16 +386,14 @@ __device__ int build_list(const PagedArgs& a, const PagedTile& w, int kv_head, i
   return min(max(all - lo, 0), count);
 }
 
-// Half i of a list: the 16 keys at i % (page_size / 16) of entry i / (page_size / 16).
-template <int PARTS>
-__device__ __forceinline__ Half list_half(const PagedArgs& a, const ListEntry<PARTS>* list, int entries, int i, int part) {
-  const int e = i >> (a.s.shift - 4);
+// Spot i of a list, of SPAN keys: those at i % (page_size / SPAN) of entry i / (page_size / SPAN).
+template <int SPAN, int PARTS>
+__device__ __forceinline__ Found list_look_up(const PagedArgs& a, const ListEntry<PARTS>* list, int entries, int i,
+                                              int part) {
+  const int per = a.s.shift - (SPAN == 16 ? 4 : SPAN == 32 ? 5 : 6);  // log2 of the spots in a page
+  const int e = i >> per;
   const ListEntry<PARTS>& entry = list[min(e, entries - 1)];
-  Half x;
-  x.page = max(uniform(entry.page), 0);
-  x.key = (uniform(entry.block) << a.s.shift) + 16 * (i & ((1 << (a.s.shift - 4)) - 1));
-  x.visible = e < entries ? static_cast<uint32_t>(uniform(static_cast<int>(entry.tokens[part]))) : 0u;
-  return x;
+  return Found{entry.page, (entry.block << a.s.shift) + SPAN * (i & ((1 << per) - 1)), e < entries ? entry.tokens[part] : 0u};
 }
 
 // Where the token kernel's keys come from.
@@ -367,12 +403,13 @@ enum Keys {
   kListSeveral // listed blocks, tiles of several tokens, which see different blocks
 };
 
-template <int D, Keys KEYS>
-__global__ __launch_bounds__(64 * token_waves<D>(), 1) void paged_token_kernel(PagedArgs a) {
+// N: spots of a tile, 1 where a page holds whole tiles.
+template <int D, Keys KEYS, int NW, int N>
+__global__ __launch_bounds__(64 * NW, 1) void paged_token_kernel(PagedArgs a) {
   constexpr bool LISTED = KEYS != kTable;
-  constexpr int NW = token_waves<D>();
   constexpr int kTile = kKeysT * 2 * D;
-  constexpr int kHalfOps = kTile / 2048;  // DMA instructions per half
+  constexpr int kSpan = kKeysT / N;           // keys of a spot
+  constexpr int kHalfOps = kTile / 2048;      // DMA instructions per 16 keys
   // The stages are variables of their own: the compiler then knows that the
   // DMA in flight into one does not write the other, and does not wait for it.
   __shared__ __attribute__((aligned(1024))) uint8_t smem0[NW][2][kTile];
@@ -380,13 +417,13 @@ __global__ __launch_bounds__(64 * token_waves<D>(), 1) void paged_token_kernel(P
   __shared__ float s_m[NW][32], s_l[NW][32];
   __shared__ ListEntry<1> s_list[LISTED ? kList : 1];
   static_assert(NW * 32 * D * 4 == sizeof(smem0), "the merge uses a stage");
-  static_assert(sizeof(smem0) >= 4 * (2 * kWords + 16), "and so does the list's scratch");
+  static_assert(!LISTED || sizeof(smem0) >= 4 * (2 * kWords + 16), "and so does the list's scratch");
   const int t_block = blockIdx.x / a.kv_heads, split = blockIdx.y;
   // the heads of each sequence and split begin on another XCD
   const int kv_head = (blockIdx.x + t_block + split) % a.kv_heads;
   PagedTile w;
   w.seq = t_block, w.tile = 0, w.tiles = 1;
-  load_range(a, w);
+  load_range(a, w);  // no groups here: the keys begin at 0
   const int r0 = 0, n_rows = min(w.lq, a.max_q) * a.group;
   if (n_rows == 0) return;
   const int here = n_rows;  // at most 32
@@ -394,26 +431,20 @@ __global__ __launch_bounds__(64 * token_waves<D>(), 1) void paged_token_kernel(P
   const int tok0 = r0 / a.group, tok1 = (r0 + here - 1) / a.group;
   const LaneRow x = lane_row(a, w, kv_head, r0 + (lane & 31), n_rows);
   const int lim_first = last_key(w, tok0);
-  const int slot = a.prefix_splits + split;
   auto empty = [&](int at) {
     if (wave == 0 && lane < here) empty_share(a, at, x.q_row, x.head);
   };
-  if (a.every_slot() && a.slots > 1 && split == 0 && w.own == 0)
-    for (int i = 0; i < a.prefix_splits; ++i) empty(i);
 
   int n_tiles, kbeg = 0, splits = 1, entries = 0;
   if (LISTED) {
     entries = uniform(build_list<64 * NW>(a, w, kv_head, r0, here, split, s_list,
                                           reinterpret_cast<uint32_t*>(&smem0[0][0][0])));
     n_tiles = ((entries << (a.s.shift - 4)) + 1) / 2;
-    if (n_tiles == 0 && a.slots > 1) return empty(slot);
+    if (n_tiles == 0 && a.slots > 1) return empty(split);
   } else {
     const int all = max(last_key(w, tok1) + 1 - w.own, 0);
     splits = (all + a.chunk - 1) / a.chunk;
-    if (split >= max(splits, a.every_slot() ? 0 : 1)) {
-      if (a.every_slot()) empty(slot);
-      return;
-    }
+    if (split >= max(splits, 1)) return;
     kbeg = w.own + split * a.chunk;
     n_tiles = (min(all - split * a.chunk, a.chunk) + kKeysT - 1) / kKeysT;
   }
@@ -429,36 +460,45 @@ __global__ __launch_bounds__(64 * token_waves<D>(), 1) void paged_token_kernel(P
     voff[i] = half_offset<D, true>(i, static_cast<int>(a.v.row_stride) * 2);
   }
   const uint32_t every = tok1 - tok0 == 31 ? ~0u : (2u << (tok1 - tok0)) - 1;
-  auto find = [&](int t, int hh) -> Half {
-    return LISTED ? list_half(a, s_list, entries, 2 * t + hh, 0) : table_half(a, table, kbeg + kKeysT * t + 16 * hh);
+  auto find = [&](int t, int i) -> Found {
+    return LISTED ? list_look_up<kSpan>(a, s_list, entries, N * t + i, 0)
+                  : look_up(a, table, kbeg + kKeysT * t + kSpan * i);
   };
-  struct Pair {
-    Half h[2];
+  auto find_all = [&](int t) {
+    FoundAll<N> p;
+#pragma unroll
+    for (int i = 0; i < N; ++i) p.at[i] = find(t, i);
+    return p;
   };
-  auto find_pair = [&](int t) { return Pair{{find(t, 0), find(t, 1)}}; };
-  auto issue = [&](uint8_t (&to)[2][kTile], const Pair& p) {
+  const int k16 = 32 * static_cast<int>(a.k.row_stride), v16 = 32 * static_cast<int>(a.v.row_stride);  // bytes of 16 rows
+  auto issue = [&](uint8_t (&to)[2][kTile], const Spots<N>& p) {
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const __amdgpu_buffer_rsrc_t kr = raw_buffer(half_base(a.k, p.h[hh], slot_mask, kv_head), 0x7fffffff);
-      const __amdgpu_buffer_rsrc_t vr = raw_buffer(half_base(a.v, p.h[hh], slot_mask, kv_head), 0x7fffffff);
+    for (int i = 0; i < N; ++i) {
+      const __amdgpu_buffer_rsrc_t kr = raw_buffer(spot_base(a.k, p.at[i], slot_mask, kv_head), 0x7fffffff);
+      const __amdgpu_buffer_rsrc_t vr = raw_buffer(spot_base(a.v, p.at[i], slot_mask, kv_head), 0x7fffffff);
 #pragma unroll
-      for (int i = 0; i < kHalfOps; ++i) dma16(kr, koff[i], 0, &to[0][1024 * (kHalfOps * hh + i)]);
+      for (int hh = 0; hh < 2 / N; ++hh) {
+        const int half = i * (2 / N) + hh;
 #pragma unroll
-      for (int i = 0; i < kHalfOps; ++i) dma16(vr, voff[i], 0, &to[1][1024 * (kHalfOps * hh + i)]);
+        for (int j = 0; j < kHalfOps; ++j) dma16(kr, koff[j], hh * k16, &to[0][1024 * (kHalfOps * half + j)]);
+#pragma unroll
+        for (int j = 0; j < kHalfOps; ++j) dma16(vr, voff[j], hh * v16, &to[1][1024 * (kHalfOps * half + j)]);
+      }
     }
   };
 
   RowState<D> st;
   st.clear();
-  Pair now, next, after;  // the tile in use, the one that is loaded, the one whose pages are looked up
+  Spots<N> now, next;  // the tile in use, the one that is loaded
+  FoundAll<N> after;   // the one behind it
   // Tile t is in one stage; the reads of the other have returned: refill it.
   auto turn = [&](uint8_t (&to)[2][kTile], int t) {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), other counters untouched
     if (t + NW < n_tiles) {
-      next = after;
+      next = to_spots(a, after);
       issue(to, next);
-      after = find_pair(min(t + 2 * NW, n_tiles - 1));
+      after = find_all(min(t + 2 * NW, n_tiles - 1));
       wait_vmcnt<4 * kHalfOps>();
     } else {
       wait_vmcnt<0>();
@@ -467,9 +507,11 @@ __global__ __launch_bounds__(64 * token_waves<D>(), 1) void paged_token_kernel(P
     __builtin_amdgcn_sched_barrier(0);
   };
   // whether every row sees all of the tile
-  auto whole = [&](const Pair& p) {
-    return p.h[0].key + 15 <= lim_first && p.h[1].key + 15 <= lim_first &&
-           (p.h[0].visible & p.h[1].visible & every) == every;
+  auto whole = [&](const Spots<N>& p) {
+    bool all = true;
+#pragma unroll
+    for (int i = 0; i < N; ++i) all &= p.at[i].key + kSpan - 1 <= lim_first && (p.at[i].visible & every) == every;
+    return all;
   };
   const int tk = static_cast<int>(x.q_row) - w.q0 - tok0;  // the lane's token
   // Tiles that end behind some row's last key may hold anything there.  Where rows differ in
@@ -477,20 +519,20 @@ __global__ __launch_bounds__(64 * token_waves<D>(), 1) void paged_token_kernel(P
   // always finite: these tiles are only looked through if an output says otherwise, in a second pass.
   bool careful = false;
   auto masked = [&](const uint8_t (&from)[2][kTile], int t) {
-    const bool ends = now.h[0].key + 15 > lim_first || now.h[1].key + 15 > lim_first;
-    Limits<1> lim;
+    bool ends = false;
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh)
-      lim.at[hh] = (now.h[hh].visible >> tk) & 1 ? x.limit - now.h[hh].key + 16 * hh : -1;
-    attend_halves<D, 1>(from[0], from[1], q, st, a.c, lim, KEYS != kListSeveral || careful || ends, a.v.row_stride,
-                        [&](int i) { return half_base(a.v, find(t, i), slot_mask, kv_head); });
+    for (int i = 0; i < N; ++i) ends |= now.at[i].key + kSpan - 1 > lim_first;
+    attend_halves<D, 1>(from[0], from[1], q, st, a.c, spot_limits<1>(now, x.limit, tk),
+                        KEYS != kListSeveral || careful || ends, a.v.row_stride, [&](int i) {
+                          return spot_base(a.v, to_spot(a, find(t, i * N / 2)), slot_mask, kv_head) + i % (2 / N) * 16 * a.v.row_stride;
+                        });
   };
   int t = wave;
   auto start = [&] {
     if (t < n_tiles) {
-      now = find_pair(t);
+      now = to_spots(a, find_all(t));
       issue(smem0[wave], now);
-      after = find_pair(min(t + NW, n_tiles - 1));
+      after = find_all(min(t + NW, n_tiles - 1));
     }
   };
   start();
@@ -517,13 +559,13 @@ __global__ __launch_bounds__(64 * token_waves<D>(), 1) void paged_token_kernel(P
     int stage = 0;
     while (t < n_tiles && whole(now)) {
       turn(smem1[wave], t);
-      attend<D, 1, false>(smem0[wave][0], smem0[wave][1], q, st, a.c, 0, false);
+      attend<D, 1, false, kKeep<D>>(smem0[wave][0], smem0[wave][1], q, st, a.c, 0, false);
       now = next;
       t += NW;
       stage = 1;
       if (t >= n_tiles || !whole(now)) break;
       turn(smem0[wave], t);
-      attend<D, 1, false>(smem1[wave][0], smem1[wave][1], q, st, a.c, 0, false);
+      attend<D, 1, false, kKeep<D>>(smem1[wave][0], smem1[wave][1], q, st, a.c, 0, false);
       now = next;
       t += NW;
       stage = 0;
@@ -573,7 +615,7 @@ __global__ __launch_bounds__(64 * token_waves<D>(), 1) void paged_token_kernel(P
     if (direct) {
       store_quad(a, q_row, head, d, o, m, l);
     } else {
-      const int64_t row = part_row(a, slot, q_row, head);
+      const int64_t row = part_row(a, split, q_row, head);
       *reinterpret_cast<f32x4*>(a.part_o + row * D + d) = o;
       if (d == 0) a.part_ml[row] = make_float2(m, l);
     }
@@ -584,34 +626,44 @@ __global__ __launch_bounds__(64 * token_waves<D>(), 1) void paged_token_kernel(P
 constexpr int kRowsP = 128;  // rows of a block: 4 waves x 32
 constexpr int kKeysP = 64;   // keys of a tile
 
-// Where the rows kernel's keys come from: the table (a sequence's own keys), the prefix
-// of a group, or listed blocks.
-enum RowKeys { kOwn, kPrefix, kListed };
-
-template <int D, RowKeys KEYS>
+// A launch has units of kv_heads blocks each: (tile, split) pairs of sequences over their
+// own keys, or over listed blocks, and behind them those of groups over their prefixes.
+// (64 single tokens behind a prefix of 16384, whole call: 101 us; prefix first 113; the kinds evenly mixed 113 to
+// 126, as a block that multiplies then waits for its keys behind those that stream the caches.)
+template <int D, bool LISTED, int N>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(PagedArgs a) {
-  constexpr bool PREFIX = KEYS == kPrefix, LISTED = KEYS == kListed;
   constexpr int kTile = kKeysP * 2 * D;
   constexpr int kOps = kTile / 4096;  // DMA instructions per wave and tile
+  constexpr int kSpan = kKeysP / N;   // keys of a spot
   // two variables: see paged_token_kernel
   __shared__ __attribute__((aligned(1024))) uint8_t smem0[2][kTile];
   __shared__ __attribute__((aligned(1024))) uint8_t smem1[2][kTile];
   __shared__ ListEntry<4> s_list[LISTED ? kList : 1];
   static_assert(sizeof(smem0) >= 4 * (2 * kWords + 16), "the list's scratch is in a stage");
-  const int kv_head = blockIdx.x % a.kv_heads, split = blockIdx.y;
+  const int kv_head = blockIdx.x % a.kv_heads;
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  int unit = blockIdx.x / a.kv_heads;
+  bool prefix = false;
+  if (!LISTED && a.prefix_units > 0) {
+    const int own = a.units - a.prefix_units;
+    prefix = unit >= own;
+    unit -= prefix ? own : 0;
+  }
+  const int tiles = prefix ? a.prefix_tiles : a.tiles;
+  const int split = uniform(unit / tiles), tile = unit - split * tiles;
   PagedTile w;
   LaneRow x;
   int r0 = 0, n_rows = 0;
   // the last key that some row of the wave sees; the last that every row of the block sees; keys of the
   // block; the last key that every row of the wave sees
   int lim_last, block_first, all, lim_first = 0;
-  if (PREFIX) {
+  if (prefix) {
     GroupRange g;
-    if (!find_group_tile(a, blockIdx.x / a.kv_heads, kRowsP, w, g)) return;
+    if (!find_group_tile(a, tile, kRowsP, w, g)) return;
     x = lane_row(a, w, kv_head, w.tile * kRowsP + 32 * wave + (lane & 31), w.lq * a.group);
-    // the row's sequence: the last one that begins at or before it
-    int lo = g.first, hi = g.past;
+    // the row's sequence: the last one that begins at or before it; often they have a row each
+    int lo = min(g.first + static_cast<int>(x.q_row) - w.q0, g.past - 1), hi = lo + 1;
+    if (a.s.cu_q[lo] > x.q_row || (hi < g.past && a.s.cu_q[hi] <= x.q_row)) lo = g.first, hi = g.past;
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (a.s.cu_q[mid] <= x.q_row) lo = mid; else hi = mid;
@@ -633,19 +685,19 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(Paged
     block_first = uniform(min(min(s_first[0], s_first[1]), min(s_first[2], s_first[3])));
     all = w.end;
   } else {
-    if (!find_tile(a, blockIdx.x / a.kv_heads, kRowsP, w)) return;
-    load_range(a, w);
+    if (!find_tile(a, tile, kRowsP, w)) return;
+    if (a.n_groups > 0) load_range(a, w);
     r0 = (w.tiles - 1 - w.tile) * kRowsP;  // the last tiles see the most keys: first
     n_rows = min(w.lq, a.max_q) * a.group;
     const int rw = r0 + 32 * wave;
     x = lane_row(a, w, kv_head, rw + (lane & 31), n_rows);
     block_first = last_key(w, r0 / a.group);
     lim_first = last_key(w, min(rw, n_rows - 1) / a.group);
-    lim_last = last_key(w, min(rw + 31, n_rows - 1) / a.group);
+    lim_last = rw < n_rows ? last_key(w, min(rw + 31, n_rows - 1) / a.group) : -1;  // a wave without rows only loads
     all = max(last_key(w, (min(r0 + kRowsP, n_rows) - 1) / a.group) + 1 - w.own, 0);
   }
-  const int chunk = PREFIX ? a.prefix_chunk : a.chunk;
-  const int slot = PREFIX ? split : a.prefix_splits + split;
+  const int chunk = prefix ? a.prefix_chunk : a.chunk;
+  const int slot = prefix ? split : a.prefix_splits + split;
   auto empty = [&](int at) {
     if (x.valid && lane < 32) empty_share(a, at, x.q_row, x.head);
   };
@@ -657,7 +709,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(Paged
     if (kend == 0 && a.slots > 1) return empty(slot);
   } else {
     splits = (all + chunk - 1) / chunk;  // that have keys to see
-    if (!PREFIX && a.n_groups > 0 && split == 0 && w.own == 0)
+    if (!prefix && a.n_groups > 0 && split == 0 && w.own == 0)
       for (int i = 0; i < a.prefix_splits; ++i) empty(i);
     if (split >= max(splits, a.n_groups > 0 ? 0 : 1)) {
       if (a.n_groups > 0) empty(slot);
@@ -680,50 +732,66 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(Paged
     koff[i] = half_offset<D, false>(D == 256 ? 4 * i + wave : in_half, static_cast<int>(a.k.row_stride) * 2);
     voff[i] = half_offset<D, true>(D == 256 ? 4 * i + wave : in_half, static_cast<int>(a.v.row_stride) * 2);
   }
-  struct Quad {
-    Half h[4];
+  auto find = [&](int key) -> Found {
+    return LISTED ? list_look_up<kSpan>(a, s_list, entries, key / kSpan, wave) : look_up(a, table, key);
   };
-  auto find = [&](int key) -> Half {
-    return LISTED ? list_half(a, s_list, entries, key >> 4, wave) : table_half(a, table, key);
+  auto find_all = [&](int key) {
+    FoundAll<N> p;
+#pragma unroll
+    for (int i = 0; i < N; ++i) p.at[i] = find(key + kSpan * i);
+    return p;
   };
-  auto find_quad = [&](int key) { return Quad{{find(key), find(key + 16), find(key + 32), find(key + 48)}}; };
-  auto issue = [&](uint8_t (&to)[2][kTile], const Quad& p) {
+  const int k16 = 32 * static_cast<int>(a.k.row_stride), v16 = 32 * static_cast<int>(a.v.row_stride);  // bytes of 16 rows
+  auto issue = [&](uint8_t (&to)[2][kTile], const Spots<N>& p) {
+    __amdgpu_buffer_rsrc_t kr, vr;
+    if (N == 1) {
+      kr = raw_buffer(spot_base(a.k, p.at[0], slot_mask, kv_head), 0x7fffffff);
+      vr = raw_buffer(spot_base(a.v, p.at[0], slot_mask, kv_head), 0x7fffffff);
+    }
 #pragma unroll
     for (int i = 0; i < kOps; ++i) {
-      // row (4 i + wave) * kRowsOp of the tile
-      Half y = p.h[4 * i * kRowsOp / 16];
-      if (D == 64 && wave >= 2) y = p.h[4 * i * kRowsOp / 16 + 1];
-      const __amdgpu_buffer_rsrc_t kr = raw_buffer(half_base(a.k, y, slot_mask, kv_head), 0x7fffffff);
-      const __amdgpu_buffer_rsrc_t vr = raw_buffer(half_base(a.v, y, slot_mask, kv_head), 0x7fffffff);
-      dma16(kr, koff[i % kSame], 0, &to[0][1024 * (4 * i + wave)]);
-      dma16(vr, voff[i % kSame], 0, &to[1][1024 * (4 * i + wave)]);
+      // row (4 i + wave) * kRowsOp of the tile is in half `half`, for heads of 64 and the upper waves one on
+      constexpr int kEach = 4 / N;  // halves of a spot
+      const int half = 4 * i * kRowsOp / 16, more = D == 64 ? wave >> 1 : 0;
+      if (N == 4 || (N == 2 && (i == 0 || half % kEach == 0))) {
+        Spot y = p.at[half / kEach];
+        if (N == 4 && more) y = p.at[half / kEach + 1];
+        kr = raw_buffer(spot_base(a.k, y, slot_mask, kv_head), 0x7fffffff);
+        vr = raw_buffer(spot_base(a.v, y, slot_mask, kv_head), 0x7fffffff);
+      }
+      dma16(kr, koff[i % kSame], N < 4 ? (half % kEach + more) * k16 : 0, &to[0][1024 * (4 * i + wave)]);
+      dma16(vr, voff[i % kSame], N < 4 ? (half % kEach + more) * v16 : 0, &to[1][1024 * (4 * i + wave)]);
     }
   };
 
   RowState<D> st;
   st.clear();
-  Quad now, next, after;  // the tile in use, the one that is loaded, the one whose pages are looked up
+  Spots<N> now, next;  // the tile in use, the one that is loaded
+  FoundAll<N> after;   // the one behind it
   // Tile `key` has arrived in one stage and every wave is done with the other: refill that.
   auto turn = [&](uint8_t (&to)[2][kTile], int key) {
     wait_vmcnt<0>();
     stage_barrier();
     if (key + kKeysP < kend) {
-      next = after;
+      next = to_spots(a, after);
       issue(to, next);
-      after = find_quad(min(key + 2 * kKeysP, kend - 1 & ~(kKeysP - 1)));
+      after = find_all(min(key + 2 * kKeysP, kend - 1 & ~(kKeysP - 1)));
     }
     __builtin_amdgcn_sched_barrier(0);
   };
   auto masked = [&](const uint8_t (&from)[2][kTile], int key, const Limits<kKeysP / 32>& lim, bool scan) {
     attend_halves<D, kKeysP / 32>(from[0], from[1], q, st, a.c, lim, scan, a.v.row_stride,
-                                  [&](int i) { return half_base(a.v, find(key + 16 * i), slot_mask, kv_head); });
+                                  [&](int i) {
+                                    return spot_base(a.v, to_spot(a, find(key + 16 * i / kSpan * kSpan)), slot_mask, kv_head) +
+                                           16 * i % kSpan * a.v.row_stride;
+                                  });
   };
   int key = kbeg;
   auto start = [&] {
     if (key < kend) {
-      now = find_quad(key);
+      now = to_spots(a, find_all(key));
       issue(smem0, now);
-      after = find_quad(key + kKeysP);
+      after = find_all(key + kKeysP);
     }
   };
   start();
@@ -731,25 +799,27 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(Paged
     const int tk = static_cast<int>(x.q_row) - w.q0 - (r0 + 32 * wave) / a.group;  // the lane's token of the wave's
     bool careful = false;  // see paged_token_kernel
     auto use = [&](const uint8_t (&from)[2][kTile], int key) {
-      if ((now.h[0].visible | now.h[1].visible | now.h[2].visible | now.h[3].visible) != 0) {
-        Limits<kKeysP / 32> lim;
-        int last = 0;
+      uint32_t any = 0;
+      int last = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          lim.at[i] = now.h[i].visible >> tk & 1 ? x.limit - now.h[i].key + 16 * i : -1;
-          last = max(last, now.h[i].key + 15);
-        }
-        masked(from, key, lim, careful || last > lim_first);
-      }
+      for (int i = 0; i < N; ++i) any |= now.at[i].visible, last = max(last, now.at[i].key + kSpan - 1);
+      if (any) masked(from, key, spot_limits<kKeysP / 32>(now, x.limit, tk), careful || last > lim_first);
       now = next;
     };
     for (;;) {
-      for (; key < kend; key += 2 * kKeysP) {
-        turn(smem1, key);
-        use(smem0, key);
-        if (key + kKeysP >= kend) break;
-        turn(smem0, key + kKeysP);
-        use(smem1, key + kKeysP);
+      if (kKeep<D>) {
+        for (; key < kend; key += 2 * kKeysP) {
+          turn(smem1, key);
+          use(smem0, key);
+          if (key + kKeysP >= kend) break;
+          turn(smem0, key + kKeysP);
+          use(smem1, key + kKeysP);
+        }
+      } else {  // one copy of the code: two need more registers than there are
+        for (int stage = 0; key < kend; key += kKeysP, stage ^= 1) {
+          turn(stage ? smem0 : smem1, key);
+          use(stage ? smem1 : smem0, key);
+        }
       }
       if (careful || !__syncthreads_or(not_finite(st))) break;
       careful = true;
@@ -758,21 +828,24 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(Paged
       start();
     }
   } else {
-    auto valid = [&](const Quad& p) {
-      return (p.h[0].visible & p.h[1].visible & p.h[2].visible & p.h[3].visible) != 0;
+    auto valid = [&](const Spots<N>& p) {
+      uint32_t all = ~0u;
+#pragma unroll
+      for (int i = 0; i < N; ++i) all &= p.at[i].visible;
+      return all != 0;
     };
     int stage = 0;
     // tiles that every row of the block sees whole, in pairs
     const int full = min(kend, block_first + 1);
     while (key + kKeysP <= full && valid(now)) {
       turn(smem1, key);
-      attend<D, kKeysP / 32, false>(smem0[0], smem0[1], q, st, a.c, 0, false);
+      if (lim_last >= 0) attend<D, kKeysP / 32, false, kKeep<D>>(smem0[0], smem0[1], q, st, a.c, 0, false);
       now = next;
       key += kKeysP;
       stage = 1;
       if (key + kKeysP > full || !valid(now)) break;
       turn(smem0, key);
-      attend<D, kKeysP / 32, false>(smem1[0], smem1[1], q, st, a.c, 0, false);
+      if (lim_last >= 0) attend<D, kKeysP / 32, false, kKeep<D>>(smem1[0], smem1[1], q, st, a.c, 0, false);
       now = next;
       key += kKeysP;
       stage = 0;
@@ -781,12 +854,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(Paged
     for (; key < kend; key += kKeysP, stage ^= 1) {
       uint8_t(&from)[2][kTile] = stage ? smem1 : smem0;
       turn(stage ? smem0 : smem1, key);
-      if (key <= lim_last) {
-        Limits<kKeysP / 32> lim;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) lim.at[i] = now.h[i].visible ? x.limit - key : -1;
-        masked(from, key, lim, true);
-      }
+      if (key <= lim_last) masked(from, key, spot_limits<kKeysP / 32>(now, x.limit, 0), true);
       now = next;
     }
   }
@@ -833,7 +901,9 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a) {
     pos = static_cast<int>(q_row - static_cast<int64_t>(seq) * a.max_q);
   } else {  // u counts q's rows: the sequence is the last one that begins at or before it
     if (q_row >= a.s.q_rows) return;
-    int lo = 0, hi = a.s.n_seqs;
+    int lo = min(static_cast<int>(q_row), a.s.n_seqs - 1), hi = a.s.n_seqs;
+    if (a.s.cu_q[lo] > q_row || (lo + 1 < hi && a.s.cu_q[lo + 1] <= q_row)) lo = 0;  // not one row each
+    else hi = lo + 1;
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (a.s.cu_q[mid] <= q_row) lo = mid; else hi = mid;
@@ -914,10 +984,13 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Plan {
   bool token;                   // the few-rows kernel: every sequence is one tile
-  int64_t tiles, prefix_tiles;  // row tiles x key heads
+  int waves;                    // of its blocks
+  int64_t tiles, prefix_tiles;  // row tiles
   int chunk, splits;            // own keys of a split (listed blocks: the fewest); splits
   int prefix_chunk, prefix_splits;
   int slots() const { return splits + prefix_splits; }
+  int64_t prefix_units() const { return prefix_tiles * prefix_splits; }
+  int64_t units() const { return tiles * splits + prefix_units(); }
 };
 
 // Tokens that a tile may hold rows of.
@@ -932,8 +1005,11 @@ int tile_tokens(int group, int max_q, bool token) {
 int64_t pick_chunk(int64_t keys, int64_t tiles, int64_t unit, int64_t want, int64_t least, int64_t most) {
   int64_t chunk = ceil_div(keys, std::max<int64_t>(1, ceil_div(want, std::max<int64_t>(tiles, 1))));
   chunk = std::min(std::max(chunk, least), most);
-  return ceil_div(chunk, unit) * unit;
+  return ceil_div(ceil_div(keys, ceil_div(keys, chunk)), unit) * unit;  // equal pieces
 }
+
+// Tiles of kRowsP rows that `rows` rows in up to `parts` sequences or groups make.
+int64_t tile_bound(int64_t rows, int64_t parts) { return (rows + (kRowsP - 1) * parts) / kRowsP; }
 
 Plan make_plan(const moe_paged_attn& d) {
   Plan p = {};
@@ -941,21 +1017,22 @@ Plan make_plan(const moe_paged_attn& d) {
   const int64_t g = s.q_heads / s.kv_heads;
   const int64_t seqs = std::min<int64_t>(s.n_seqs, s.q_rows);
   const bool listed = d.n_blocks > 0, grouped = d.n_groups > 0;
-  p.token = d.max_q * g <= kRowsT;
-  p.tiles = (p.token ? s.n_seqs : seqs + s.q_rows * g / kRowsP) * s.kv_heads;
-  const int64_t tiles = std::max<int64_t>(p.tiles, 1);
+  p.token = d.max_q * g <= kRowsT && !grouped;
+  p.tiles = p.token ? s.n_seqs : tile_bound(s.q_rows * g, seqs);
+  const int64_t tiles = std::max<int64_t>(p.tiles * s.kv_heads, 1);
   int64_t keys = std::max(d.max_kv, 1);
   if (grouped) keys += s.page_size - 1;  // what is left of the prefix's last page
   if (listed)
     keys = std::max<int64_t>(1, std::min<int64_t>(static_cast<int64_t>(tile_tokens(g, d.max_q, p.token)) * d.n_blocks,
                                                   ceil_div(keys, s.page_size))) * s.page_size;
-  const int64_t unit = p.token ? kKeysT * (s.head_dim == 256 ? 2 : 4) : kKeysP;
+  p.waves = s.head_dim == 256 || tiles >= 2 * kCus ? 2 : 4;
+  const int64_t unit = p.token ? kKeysT * p.waves : kKeysP;
   const int64_t want = s.head_dim > (p.token ? 64 : 128) ? kCus : 2 * kCus;
   const int64_t least = p.token ? (keys <= 4 * unit ? 4 : 2) * unit
                                 : std::min(std::max(tiles / 16, int64_t{4}), int64_t{16}) * unit;
-  const int64_t most = !p.token || listed ? INT32_MAX
+  const int64_t most = grouped && d.max_q * g <= kRowsT ? 16 * unit : !p.token || listed ? INT32_MAX
                                 : std::max(16 * unit, ceil_div(keys, std::max(kRounds * kCus / tiles, int64_t{1})));
-  const int64_t chunk = pick_chunk(keys, p.tiles, unit, want, least, most);
+  const int64_t chunk = pick_chunk(keys, tiles, unit, want, least, most);
   if (listed) {
     // How many blocks a tile's tokens list together is known to the kernel alone: as many as one
     // of them at least, and hardly more where they agree.
@@ -968,9 +1045,15 @@ Plan make_plan(const moe_paged_attn& d) {
     p.splits = static_cast<int>(ceil_div(keys, chunk));
   }
   if (grouped && d.max_prefix >= s.page_size) {
-    p.prefix_tiles = (std::min<int64_t>(d.n_groups, s.q_rows) + s.q_rows * g / kRowsP) * s.kv_heads;
-    const int64_t piece = pick_chunk(d.max_prefix, p.prefix_tiles, kKeysP, s.head_dim > 128 ? kCus : 2 * kCus,
-                                     std::min(std::max(p.prefix_tiles / 16, int64_t{4}), int64_t{16}) * kKeysP, 1 << 30);
+    p.prefix_tiles = tile_bound(s.q_rows * g, std::min<int64_t>(d.n_groups, s.q_rows));
+    const int64_t blocks = p.prefix_tiles * s.kv_heads, row_bytes = int64_t{8} * s.q_rows * s.q_heads * s.head_dim;
+    int64_t fill = kCus;
+    if (s.head_dim <= 128) {
+      const int64_t splits = std::max<int64_t>(kCus / std::max<int64_t>(blocks, 1), 1), steps = blocks * ceil_div(d.max_prefix, kKeysP);
+      if (steps / kCus * 400 > splits * row_bytes / 5000) fill = 2 * kCus;
+    }
+    const int64_t piece = pick_chunk(d.max_prefix, blocks, kKeysP, fill,
+                                     std::min(std::max(blocks / 16, 4), int64_t{16}) * kKeysP, 1 << 30);
     p.prefix_chunk = static_cast<int>(piece);
     p.prefix_splits = static_cast<int>(ceil_div(d.max_prefix, piece));
   }
@@ -998,27 +1081,46 @@ int check_shape(const moe_paged_attn* a) {
   if (a->n_blocks > 0 && a->max_kv > static_cast<int64_t>(32 * kWords) * a->p.page_size) return MOE_ESHAPE;
   const Plan p = make_plan(*a);
   // grid limits: 2^32 threads along x, 65535 blocks along y
-  if (p.tiles > 0xffffff || p.prefix_tiles > 0xffffff || p.splits > 65535 || p.prefix_splits > 65535) return MOE_ESHAPE;
+  if (p.units() > 0xffffff / a->p.kv_heads || p.splits > 65535) return MOE_ESHAPE;
   if (static_cast<int64_t>(a->p.q_rows) * a->p.q_heads > 0x3fffffff) return MOE_ESHAPE;
   return MOE_OK;
 }
 
+template <int D, int NW, int N>
+void launch_token(const PagedArgs& a, dim3 grid, hipStream_t s) {
+  if (!a.n_blocks)
+    paged_token_kernel<D, kTable, NW, N><<<grid, 64 * NW, 0, s>>>(a);
+  else if (a.max_q == 1)
+    paged_token_kernel<D, kListOne, NW, N><<<grid, 64 * NW, 0, s>>>(a);
+  else
+    paged_token_kernel<D, kListSeveral, NW, N><<<grid, 64 * NW, 0, s>>>(a);
+}
+
+template <int D, int N>
+void launch_rows(const PagedArgs& a, unsigned blocks, hipStream_t s) {
+  if (a.n_blocks)
+    paged_rows_kernel<D, true, N><<<blocks, 256, 0, s>>>(a);
+  else
+    paged_rows_kernel<D, false, N><<<blocks, 256, 0, s>>>(a);
+}
+
 template <int D>
 void launch(const PagedArgs& a, const Plan& p, hipStream_t s) {
-  if (p.prefix_splits)
-    paged_rows_kernel<D, kPrefix><<<dim3(static_cast<unsigned>(p.prefix_tiles), static_cast<unsigned>(p.prefix_splits)),
-                                 256, 0, s>>>(a);
-  const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>(p.splits));
-  if (!p.token && a.n_blocks)
-    paged_rows_kernel<D, kListed><<<grid, 256, 0, s>>>(a);
-  else if (!p.token)
-    paged_rows_kernel<D, kOwn><<<grid, 256, 0, s>>>(a);
-  else if (!a.n_blocks)
-    paged_token_kernel<D, kTable><<<grid, 64 * token_waves<D>(), 0, s>>>(a);
-  else if (a.max_q == 1)
-    paged_token_kernel<D, kListOne><<<grid, 64 * token_waves<D>(), 0, s>>>(a);
-  else
-    paged_token_kernel<D, kListSeveral><<<grid, 64 * token_waves<D>(), 0, s>>>(a);
+  if (p.token) {
+    const dim3 grid(static_cast<unsigned>(p.tiles * a.kv_heads), static_cast<unsigned>(p.splits));
+    const bool whole = 1 << a.s.shift >= kKeysT;
+    if (p.waves == 2)
+      whole ? launch_token<D, 2, 1>(a, grid, s) : launch_token<D, 2, 2>(a, grid, s);
+    else if (D < 256)
+      whole ? launch_token<D, D < 256 ? 4 : 2, 1>(a, grid, s) : launch_token<D, D < 256 ? 4 : 2, 2>(a, grid, s);
+  } else {
+    const unsigned blocks = static_cast<unsigned>(p.units() * a.kv_heads);
+    switch (a.s.shift) {
+      case 4: launch_rows<D, 4>(a, blocks, s); break;
+      case 5: launch_rows<D, 2>(a, blocks, s); break;
+      default: launch_rows<D, 1>(a, blocks, s); break;
+    }
+  }
   if (a.slots > 1) {
     const int64_t rows = (a.token ? static_cast<int64_t>(a.s.n_seqs) * a.max_q : a.s.q_rows) * a.q_heads;
     paged_join_kernel<D><<<static_cast<unsigned>(ceil_div(rows, a.join_rows)), 256, 0, s>>>(a);
@@ -1069,6 +1171,8 @@ int moe_paged_attention(const moe_paged_attn* a, void* ws, size_t ws_bytes, void
   k.max_kv = std::min(a->max_kv, k.s.capacity), k.max_prefix = std::min(a->max_prefix, k.s.capacity);
   k.chunk = plan.chunk, k.splits = plan.splits, k.prefix_chunk = plan.prefix_chunk, k.prefix_splits = plan.prefix_splits;
   k.slots = plan.slots();
+  k.tiles = static_cast<int>(plan.tiles), k.prefix_tiles = static_cast<int>(plan.prefix_tiles);
+  k.units = static_cast<int>(plan.units()), k.prefix_units = static_cast<int>(plan.prefix_units());
   k.token = plan.token;
   k.tile_rows = plan.token ? moe::kRowsT : moe::kRowsP;
   k.join_rows = plan.slots() > moe::kJoinShared ? 1 : 256 / (p.head_dim / 4);

@@ -19,6 +19,24 @@ struct PagedSeqs {
 typedef const __attribute__((address_space(4))) int32_t* ConstInts;
 __device__ __forceinline__ ConstInts const_ints(const int32_t* p) { return (ConstInts)p; }
 
+// Inclusive prefix sum over the 64 lanes of a wave, in the vector unit alone: every
+// block of these kernels looks its work up, before it can load anything.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_or_zero(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 15, false);
+}
+__device__ __forceinline__ int wave_prefix(int v) {
+  v += dpp_or_zero<0x111, 15>(v);  // row_shr 1, 2, 4, 8: inside 16 lanes
+  v += dpp_or_zero<0x112, 15>(v);
+  v += dpp_or_zero<0x114, 15>(v);
+  v += dpp_or_zero<0x118, 15>(v);
+  v += dpp_or_zero<0x142, 10>(v);  // lane 15 of rows 0 and 2 to rows 1 and 3
+  v += dpp_or_zero<0x143, 12>(v);  // lane 31 to rows 2 and 3
+  return v;
+}
+// The value of a lane that all lanes name.
+__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
 __host__ inline bool paged_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 inline int check_paged_heads(const moe_heads& h) {
