@@ -1017,7 +1017,8 @@ Plan make_plan(const moe_paged_attn& d) {
   const int64_t g = s.q_heads / s.kv_heads;
   const int64_t seqs = std::min<int64_t>(s.n_seqs, s.q_rows);
   const bool listed = d.n_blocks > 0, grouped = d.n_groups > 0;
-  p.token = d.max_q * g <= kRowsT && !grouped;
+  const bool few = d.max_q * g <= kRowsT;
+  p.token = few && !grouped;
   p.tiles = p.token ? s.n_seqs : tile_bound(s.q_rows * g, seqs);
   const int64_t tiles = std::max<int64_t>(p.tiles * s.kv_heads, 1);
   int64_t keys = std::max(d.max_kv, 1);
@@ -1030,8 +1031,8 @@ Plan make_plan(const moe_paged_attn& d) {
   const int64_t want = s.head_dim > (p.token ? 64 : 128) ? kCus : 2 * kCus;
   const int64_t least = p.token ? (keys <= 4 * unit ? 4 : 2) * unit
                                 : std::min(std::max(tiles / 16, int64_t{4}), int64_t{16}) * unit;
-  const int64_t most = grouped && d.max_q * g <= kRowsT ? 16 * unit : !p.token || listed ? INT32_MAX
-                                : std::max(16 * unit, ceil_div(keys, std::max(kRounds * kCus / tiles, int64_t{1})));
+  const int64_t most = !few || listed ? INT32_MAX
+                                      : std::max(16 * unit, ceil_div(keys, std::max(kRounds * kCus / tiles, int64_t{1})));
   const int64_t chunk = pick_chunk(keys, tiles, unit, want, least, most);
   if (listed) {
     // How many blocks a tile's tokens list together is known to the kernel alone: as many as one
@@ -1053,7 +1054,7 @@ Plan make_plan(const moe_paged_attn& d) {
       if (steps / kCus * 400 > splits * row_bytes / 5000) fill = 2 * kCus;
     }
     const int64_t piece = pick_chunk(d.max_prefix, blocks, kKeysP, fill,
-                                     std::min(std::max(blocks / 16, 4), int64_t{16}) * kKeysP, 1 << 30);
+                                     std::min(std::max(blocks / 16, int64_t{4}), int64_t{16}) * kKeysP, 1 << 30);
     p.prefix_chunk = static_cast<int>(piece);
     p.prefix_splits = static_cast<int>(ceil_div(d.max_prefix, piece));
   }
