@@ -46,16 +46,22 @@ struct PagedArgs {
 };
 
 // ---------------------------------------------------------------- work
+// A lane's group of the first 64, loaded before anything is known.
+struct LaneGroup {
+  GroupRange range;
+  int prefix;
+};
+__device__ __forceinline__ LaneGroup lane_group(const PagedArgs& a, int base) {
+  const int g = min(base + static_cast<int>(threadIdx.x & 63), a.n_groups - 1);
+  return LaneGroup{group_range(a.cu_group, g, a.s.n_seqs), a.prefix_len[g]};
+}
 // The prefix length that sequence b's group names (0 without one): the last group that
-// begins at or before b.  For a whole wave, 64 groups at a time.
-__device__ int prefix_of(const PagedArgs& a, int b) {
-  const int lane = threadIdx.x & 63;
+// begins at or before b.  For a whole wave, 64 groups at a time; mine: the first of them.
+__device__ __forceinline__ int prefix_of(const PagedArgs& a, int b, LaneGroup mine) {
   for (int base = 0; base < a.n_groups; base += 64) {
-    const int g = min(base + lane, a.n_groups - 1);
-    const GroupRange r = group_range(a.cu_group, g, a.s.n_seqs);
-    const int len = a.prefix_len[g];
-    const uint64_t mine = __ballot(b >= r.first && b < r.past);
-    if (mine) return lane_value(len, 63 - __clzll(static_cast<long long>(mine)));
+    if (base > 0) mine = lane_group(a, base);
+    const uint64_t holds = __ballot(b >= mine.range.first && b < mine.range.past);
+    if (holds) return lane_value(mine.prefix, 63 - __clzll(static_cast<long long>(holds)));
   }
   return 0;
 }
@@ -90,13 +96,6 @@ __device__ bool find_tile(const PagedArgs& a, int t, int rows, PagedTile& w) {
     t -= lane_value(incl, 63);
   }
   return false;
-}
-
-// The range of a sequence behind its group's prefix.
-__device__ __forceinline__ void load_range(const PagedArgs& a, PagedTile& w) {
-  const PagedRange r = sequence(a, w.seq, prefix_of(a, w.seq));
-  w.q0 = uniform(r.q0), w.lq = uniform(r.lq), w.diag = uniform(r.diag);
-  w.own = uniform(r.own), w.end = uniform(r.end);
 }
 
 // Tile t over all groups: 128-row tiles of the rows of a group's sequences, in groups
@@ -423,7 +422,9 @@ __global__ __launch_bounds__(64 * NW, 1) void paged_token_kernel(PagedArgs a) {
   const int kv_head = (blockIdx.x + t_block + split) % a.kv_heads;
   PagedTile w;
   w.seq = t_block, w.tile = 0, w.tiles = 1;
-  load_range(a, w);  // no groups here: the keys begin at 0
+  const PagedRange range = sequence(a, w.seq, 0);  // no groups here: the keys begin at 0
+  w.q0 = uniform(range.q0), w.lq = uniform(range.lq), w.diag = uniform(range.diag);
+  w.own = 0, w.end = uniform(range.end);
   const int r0 = 0, n_rows = min(w.lq, a.max_q) * a.group;
   if (n_rows == 0) return;
   const int here = n_rows;  // at most 32
@@ -663,12 +664,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(Paged
     x = lane_row(a, w, kv_head, w.tile * kRowsP + 32 * wave + (lane & 31), w.lq * a.group);
     // the row's sequence: the last one that begins at or before it; often they have a row each
     int lo = min(g.first + static_cast<int>(x.q_row) - w.q0, g.past - 1), hi = lo + 1;
-    if (a.s.cu_q[lo] > x.q_row || (hi < g.past && a.s.cu_q[hi] <= x.q_row)) lo = g.first, hi = g.past;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (a.s.cu_q[mid] <= x.q_row) lo = mid; else hi = mid;
+    PagedRange s = sequence(a, lo, 0);
+    if (x.q_row < s.q0 || (hi < g.past && x.q_row >= s.q0 + s.lq)) {
+      lo = g.first, hi = g.past;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (a.s.cu_q[mid] <= x.q_row) lo = mid; else hi = mid;
+      }
+      s = sequence(a, lo, 0);
     }
-    const PagedRange s = sequence(a, lo, 0);
     const int pos = static_cast<int>(x.q_row) - s.q0;
     x.limit = min(pos + s.diag, w.end - 1);
     if (pos < 0 || pos >= min(s.lq, a.max_q)) x.valid = false, x.limit = w.end - 1;
@@ -685,8 +689,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(Paged
     block_first = uniform(min(min(s_first[0], s_first[1]), min(s_first[2], s_first[3])));
     all = w.end;
   } else {
+    LaneGroup mine = {};
+    if (a.n_groups > 0) mine = lane_group(a, 0);
     if (!find_tile(a, tile, kRowsP, w)) return;
-    if (a.n_groups > 0) load_range(a, w);
+    if (a.n_groups > 0) behind_prefix(w, prefix_of(a, w.seq, mine), a.max_prefix, a.max_kv, a.s.capacity, a.s.shift);
     r0 = (w.tiles - 1 - w.tile) * kRowsP;  // the last tiles see the most keys: first
     n_rows = min(w.lq, a.max_q) * a.group;
     const int rw = r0 + 32 * wave;

@@ -21,6 +21,13 @@ __host__ __device__ inline int shared_keys(int prefix_len, int max_prefix, int p
   return min_of(max_of(prefix_len, 0), max_prefix) >> page_shift << page_shift;
 }
 
+// The keys of a sequence (rows and diag are set) behind its prefix.
+__host__ __device__ inline void behind_prefix(PagedRange& s, int prefix, int max_prefix, int max_kv, int capacity,
+                                              int page_shift) {
+  s.own = shared_keys(prefix, max_prefix, page_shift);
+  s.end = min_of(s.diag + s.lq, min_of(capacity, min_of(max_of(prefix, 0), max_prefix) + max_kv));
+}
+
 // Sequence b, whose group's prefix_len is `prefix` (0: no group).  capacity =
 // table_pages * page_size; max_prefix, max_kv <= capacity < 2^30.  Both ends of
 // the rows are cut before one is taken from the other: the difference of two
@@ -31,10 +38,8 @@ __host__ __device__ inline PagedRange paged_range(const int32_t* cu_q, const int
   PagedRange s;
   s.q0 = min_of(max_of(cu_q[b], 0), q_rows);
   s.lq = min_of(max_of(cu_q[b + 1], s.q0), q_rows) - s.q0;
-  const int lk = max_of(kv_len[b], 0);
-  s.diag = lk - s.lq;
-  s.own = shared_keys(prefix, max_prefix, page_shift);
-  s.end = min_of(lk, min_of(capacity, min_of(max_of(prefix, 0), max_prefix) + max_kv));
+  s.diag = max_of(kv_len[b], 0) - s.lq;
+  behind_prefix(s, prefix, max_prefix, max_kv, capacity, page_shift);
   return s;
 }
 
