@@ -12,6 +12,9 @@ prompts, single tokens, or a mixture.  `AttentionBlock.forward` then only
 enqueues kernels on the current stream, so a single-token step and
 `Plan.advance` can be captured into a HIP graph and replayed once per token.
 
+`PagedAttentionBlock` is the same over a cache in pages (the operators of `paged`): sequences take
+pages as they grow, share those of a common prefix, and can attend to selected pages alone.
+
 `python -m mxfp4_routed_expert_moe_amd.block` runs a small decoder block: three
 prompts, then single-token steps, eager and as a graph.
 """
@@ -20,6 +23,7 @@ from __future__ import annotations
 import torch
 
 from . import attention as A
+from . import paged as P
 
 
 class Plan:
@@ -139,13 +143,16 @@ class AttentionBlock:
         self._unrun = [[] for _ in range(max_seqs)]  # the numbers of the plans that have not run
         self._since = [0] * max_seqs  # plans up to this number ended with a reset
         self._plans = 0
-        self.cache = torch.empty((max_seqs * max_len, 2 * kv_heads, head_dim), dtype=bf16, device=dev)
-        self.kv_start = torch.arange(0, max_seqs * max_len, max_len, dtype=torch.int32, device=dev)
+        self._make_cache(dev)
         self.qkv = torch.empty((max_tokens, q_heads + 2 * kv_heads, head_dim), dtype=bf16, device=dev)
         self.o = torch.empty((max_tokens, q_heads, head_dim), dtype=bf16, device=dev)
         self.y = torch.empty((max_tokens, self.hidden), dtype=bf16, device=dev)
         self.ws = A.fp8_linear_workspace(max_tokens, max(w_qkv.shape[0], self.hidden),
                                          max(self.hidden, w_out.shape[1]), dev)
+
+    def _make_cache(self, dev):
+        self.cache = torch.empty((self.max_seqs * self.max_len, 2 * self.Hkv, self.D), dtype=torch.bfloat16, device=dev)
+        self.kv_start = torch.arange(0, self.max_seqs * self.max_len, self.max_len, dtype=torch.int32, device=dev)
 
     def held(self, b: int) -> int:
         """Tokens of sequence b that count for the next plan: those of all plans made so
@@ -180,6 +187,7 @@ class AttentionBlock:
             max_kv = longest
         if not longest <= max_kv <= self.max_len:
             raise ValueError(f"max_kv must be {longest} to {self.max_len}, got {max_kv}")
+        self._reserve(new, ends, max_kv - longest)
         cu, pos, rows, last = [0], [], [], []
         for b, n in enumerate(new):
             cu.append(cu[-1] + n)
@@ -197,6 +205,10 @@ class AttentionBlock:
                 self.lens[b], self._announced[b], self._owner[b] = ends[b], None, self._plans
                 self._unrun[b].append(self._plans)
         return plan
+
+    def _reserve(self, new, ends, more):
+        """Room in the cache for sequences that grow to `ends`, and by up to `more` tokens in steps of
+        an advanced plan: every sequence has its max_len rows."""
 
     def workspace(self, plan: Plan):
         """The attention workspace of a plan, for callers that keep it."""
@@ -233,6 +245,165 @@ class AttentionBlock:
         A.attention(q, self.cache[:, :Hkv], self.cache[:, Hkv:], plan.cu_q, plan.max_q,
                     kv_start=self.kv_start[:plan.cu_q.numel() - 1], kv_len=plan.kv_len, max_kv=plan.max_kv, out=o,
                     ws=ws)
+        return A.fp8_linear(o.view(T, -1), self.w_out, self.out_scale, y=y, ws=self.ws)
+
+
+class PagedAttentionBlock(AttentionBlock):
+    """AttentionBlock over a cache of n_pages pages of page_size tokens.
+
+    A plan gives its sequences the pages that they will fill (those of an advanced plan for
+    all of its steps), `reset` gives them back, `fork` lets a sequence begin as another one, in the
+    same pages.  Neighbouring sequences that share pages are attended to as a group: what they
+    share is read once for all of them.
+
+    select (n_blocks, first, last): single-token plans attend to n_blocks pages of each sequence,
+    its first and last ones and those whose keys' bounds promise the most; None: to everything."""
+
+    def __init__(self, *args, page_size: int = 64, n_pages: int, select=None, **kw):
+        self.page_size, self.n_pages, self.select = page_size, n_pages, select
+        super().__init__(*args, **kw)
+
+    def _make_cache(self, dev):
+        if self.page_size not in (16, 32, 64, 128):
+            raise ValueError(f"page_size must be 16, 32, 64 or 128, got {self.page_size}")
+        if self.n_pages < 1:
+            raise ValueError(f"n_pages must be positive, got {self.n_pages}")
+        if self.select is not None:
+            n, first, last = self.select
+            if not (0 <= first and 1 <= last and first + last <= n <= 1024):
+                raise ValueError(f"select must be (n_blocks, first, last) with first + last <= n_blocks <= 1024, got {self.select}")
+        bf16, Hkv, D = torch.bfloat16, self.Hkv, self.D
+        self.cache = torch.zeros((self.n_pages, self.page_size, 2 * Hkv, D), dtype=bf16, device=dev)
+        self.k_pages, self.v_pages = self.cache[:, :, :Hkv], self.cache[:, :, Hkv:]
+        self.bounds = None if self.select is None else torch.zeros((self.n_pages, 2, Hkv, D), dtype=bf16, device=dev)
+        self.table = torch.full((self.max_seqs, -(-self.max_len // self.page_size)), -1, dtype=torch.int32, device=dev)
+        self.pages = [[] for _ in range(self.max_seqs)]  # of every sequence, in order
+        self.free = list(range(self.n_pages - 1, -1, -1))
+        self.users = [0] * self.n_pages  # sequences that hold a page
+        if self.select is not None:
+            self.blocks = torch.empty((self.max_tokens, Hkv, self.select[0]), dtype=torch.int32, device=dev)
+
+    def _reserve(self, new, ends, more):
+        more = 0 if any(n > 1 for n in new) else more  # only single-token plans are advanced
+        grow = [(b, -(-min(e + more, self.max_len) // self.page_size) - len(self.pages[b]))
+                for b, (n, e) in enumerate(zip(new, ends)) if n]
+        need = sum(max(n, 0) for _, n in grow)
+        if need > len(self.free):
+            raise ValueError(f"the plan needs {need} more pages, {len(self.free)} are free")
+        for b, n in grow:
+            if n > 0:
+                self._take(b, [self.free.pop() for _ in range(n)])
+
+    def _take(self, b, pages):
+        """These pages are the next ones of sequence b."""
+        have = len(self.pages[b])
+        for page in pages:
+            self.users[page] += 1
+        self.pages[b] += pages
+        self.table[b, have:have + len(pages)] = torch.tensor(pages, dtype=torch.int32, device=self.table.device)
+
+    def reset(self, b=None):
+        super().reset(b)
+        for s in range(self.max_seqs) if b is None else (b,):
+            for page in self.pages[s]:
+                self.users[page] -= 1
+                if not self.users[page]:
+                    self.free.append(page)
+            self.pages[s] = []
+            self.table[s].fill_(-1)
+
+    def fork(self, src: int, dst: int):
+        """Sequence dst, which holds nothing, begins as a copy of what src holds: in the same pages, but for
+        the last one where it is not full (a copy on the current stream).  The plans of src have run."""
+        for b in (src, dst):
+            if not 0 <= b < self.max_seqs:
+                raise ValueError(f"there are {self.max_seqs} sequences, got {b}")
+        if self.lens[dst] or self._unrun[dst] or self.pages[dst]:
+            raise ValueError(f"sequence {dst} holds tokens, or has plans: reset it first")
+        if self._unrun[src]:
+            raise ValueError(f"a plan of sequence {src} has not run: run it, or cancel it")
+        held = self.held(src)
+        full, rest = divmod(held, self.page_size)
+        if rest and not self.free:
+            raise ValueError("no page is free for a copy of the last one")
+        if full:
+            self._take(dst, self.pages[src][:full])
+        if rest:
+            page, old = self.free.pop(), self.pages[src][full]
+            self._take(dst, [page])
+            self.cache[page].copy_(self.cache[old])
+            if self.bounds is not None:
+                self.bounds[page].copy_(self.bounds[old])
+        self.lens[dst] = held
+
+    def plan(self, new, max_kv=None) -> Plan:
+        plan = super().plan(new, max_kv)
+        cu, prefix = self._groups(plan._sequences(), len(plan.new))
+        more = 0 if plan.max_q > 1 else plan.max_kv - plan.longest
+        of = {}
+        for i, j, p in zip(cu, cu[1:], prefix):
+            of.update(dict.fromkeys(range(i, j), p))
+        plan.max_prefix = max(prefix, default=0)
+        plan.max_own = max((min(self.lens[b] + more, self.max_len) - of[b] for b in plan._sequences()), default=0)
+        plan.group = None
+        if plan.max_prefix:
+            i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=self.cache.device)  # noqa: E731
+            plan.group = i32(cu), i32(prefix)
+        return plan
+
+    def _groups(self, seqs, end):
+        """Neighbours among the sequences `seqs` whose first pages are the same: where the groups begin (and the
+        last one ends, `end`), and the tokens that each shares.  A sequence joins the group before it unless
+        that takes away more than half of what the group shares."""
+        cu, shared = [], []
+        for b in seqs:
+            same = 0
+            if cu:
+                for x, y in zip(self.pages[b], self.pages[cu[-1]]):
+                    if x != y:
+                        break
+                    same += 1
+            if same and (shared[-1] is None or 2 * same >= shared[-1]):
+                shared[-1] = same if shared[-1] is None else min(same, shared[-1])
+            else:
+                cu.append(b)
+                shared.append(None)  # alone
+        return cu + [end], [(n or 0) * self.page_size for n in shared]
+
+    def workspace(self, plan: Plan):
+        """The workspaces of a plan's selection and attention, for callers that keep them."""
+        n = plan.rows.numel()
+        q, seqs = self.qkv[:n, :self.Hq], plan.cu_q.numel() - 1
+        if self._selects(plan):
+            return (P.select_blocks_workspace(q, self.bounds, seqs, plan.max_q, plan.max_kv, self.page_size),
+                    P.paged_attention_workspace(q, self.k_pages, seqs, plan.max_q, plan.max_kv, n_blocks=self.select[0]))
+        groups = 0 if plan.group is None else plan.group[1].numel()
+        return None, P.paged_attention_workspace(q, self.k_pages, seqs, plan.max_q, plan.max_own, n_groups=groups,
+                                                 max_prefix=plan.max_prefix)
+
+    def _selects(self, plan):
+        return self.select is not None and plan.max_q == 1
+
+    def _enqueue(self, x, plan: Plan, ws):
+        T, Hq, Hkv = plan.rows.numel(), self.Hq, self.Hkv
+        qkv, o, y = self.qkv[:T], self.o[:T], self.y[:T]
+        q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+        select_ws, attention_ws = ws or (None, None)
+        n = plan.cu_q.numel() - 1
+        at = plan.cu_q, plan.kv_len, self.table[:n]
+        A.fp8_linear(x, self.w_qkv, self.qkv_scale, y=qkv.view(T, -1), ws=self.ws)
+        P.paged_append(k, v, self.k_pages, self.v_pages, *at, q=q, q_out=q, bounds=self.bounds, q_weight=self.q_weight,
+                       k_weight=self.k_weight, cos_sin=self.cos_sin, **self.rope)
+        if self._selects(plan):
+            blocks = self.blocks[:T]
+            count, first, last = self.select
+            P.select_blocks(q, self.bounds, *at, 1, plan.max_kv, self.page_size, count, first=first, last=last, blocks=blocks,
+                            ws=select_ws)
+            P.paged_attention(q, self.k_pages, self.v_pages, *at, 1, plan.max_kv, blocks=blocks, out=o, ws=attention_ws)
+        else:
+            cu, prefix = plan.group or (None, None)
+            P.paged_attention(q, self.k_pages, self.v_pages, *at, plan.max_q, plan.max_own, cu_group=cu, prefix_len=prefix,
+                              max_prefix=plan.max_prefix, out=o, ws=attention_ws)
         return A.fp8_linear(o.view(T, -1), self.w_out, self.out_scale, y=y, ws=self.ws)
 
 
@@ -322,8 +493,59 @@ def example(hidden=1024, q_heads=8, kv_heads=2, head_dim=128, n_experts=16, inte
     return eager, replayed
 
 
+def paged_example(hidden=1024, q_heads=8, kv_heads=2, head_dim=128, prompt=300, samples=4, steps=6, select=None, seed=7):
+    """One prompt continued several times, over a cache in pages: the prompt runs once, the other sequences fork from
+    it, and single-token steps attend to the pages that they share once for all.
+    -> (outputs of the eager steps, outputs of a graph's replays)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda *shape: torch.randn(shape, generator=g, device="cuda")  # noqa: E731
+    w_qkv = quantise_weight(rand((q_heads + 2 * kv_heads) * head_dim, hidden) * hidden ** -0.5)
+    w_out = quantise_weight(rand(hidden, q_heads * head_dim) * (q_heads * head_dim) ** -0.5)
+    weights = 1 + 0.1 * rand(2, head_dim)
+    cos_sin = rope_table(1024, head_dim)
+    x0, x1 = rand(prompt, hidden).bfloat16(), rand(samples, hidden).bfloat16()
+
+    def build():
+        attn = PagedAttentionBlock(*w_qkv, *w_out, q_heads, kv_heads, head_dim, cos_sin, weights[0], weights[1],
+                                   max_seqs=samples, max_len=1024, max_tokens=prompt, page_size=32, n_pages=64, select=select)
+        attn.forward(x0, attn.plan([prompt]))
+        for b in range(1, samples):
+            attn.fork(0, b)
+        step = attn.plan([1] * samples, max_kv=prompt + steps)
+        return attn, step, attn.workspace(step)
+
+    attn, step, ws = build()
+    eager, x = [], x1
+    for _ in range(steps):
+        x = x + attn.forward(x, step, ws)
+        step.advance()
+        eager.append(x)
+
+    attn, step, ws = build()
+    replayed, x = [], x1.clone()
+    start = [t.clone() for t in (x, step.counts, step.rows)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # one step outside the graph: the library loads its kernels
+        attn.forward(x, step, ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x.add_(attn.forward(x, step, ws))
+        step.advance()  # counts the first replay
+    for t, v in zip((x, step.counts, step.rows), start):
+        t.copy_(v)
+    step.replayed(steps - 1)
+    for _ in range(steps):
+        graph.replay()
+        replayed.append(x.clone())
+    torch.cuda.synchronize()
+    return eager, replayed
+
+
 if __name__ == "__main__":
-    eager, replayed = example()
-    for i, (a, b) in enumerate(zip(eager, replayed)):
-        print(f"step {i}: {tuple(a.shape)} {a.dtype}, |y| {a.float().norm():.3f}; graph replay "
-              + ("bit-identical" if torch.equal(a, b) else f"off by {(a.float() - b.float()).abs().max():.3g}"))
+    for name, run in (("cache of rows", example), ("cache of pages, one prompt", paged_example),
+                      ("cache of pages, selected", lambda: paged_example(select=(6, 1, 2)))):
+        for i, (a, b) in enumerate(zip(*run())):
+            print(f"{name}, step {i}: {tuple(a.shape)} {a.dtype}, |y| {a.float().norm():.3f}; graph replay "
+                  + ("bit-identical" if torch.equal(a, b) else f"off by {(a.float() - b.float()).abs().max():.3g}"))

@@ -1,0 +1,226 @@
+"""The bookkeeping of PagedAttentionBlock on the CPU: stand-ins for the operators carry a token's number from x
+to its slot, and every call is checked for what its attention reads through the page table: token j of a
+sequence at position j, none missing, the same through the group's first sequence for what a group shares."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from mxfp4_routed_expert_moe_amd import block as K  # noqa: E402
+
+HQ, HKV, D, HIDDEN = 2, 1, 8, 32
+
+
+class Model:
+    """A block and what was fed to it."""
+
+    def __init__(self, monkeypatch, max_seqs=4, max_len=200, max_tokens=300, n_pages=40, page_size=16, select=None):
+        self.calls = []
+
+        def linear(x, w, scale, y=None, ws=None):
+            y[:] = x[:, :1]
+            return y
+
+        def append(k, v, k_pages, v_pages, cu_q, kv_len, table, **kw):
+            for b in range(len(kv_len)):
+                n = int(cu_q[b + 1] - cu_q[b])
+                for i in range(n):
+                    p = int(kv_len[b]) - n + i
+                    page = int(table[b, p // page_size]) if p // page_size < table.shape[1] else -1
+                    if page >= 0:
+                        k_pages[page, p % page_size] = k[cu_q[b] + i]
+            return kw["q_out"]
+
+        def attention(q, k_pages, v_pages, cu_q, kv_len, table, max_q, max_kv, *, cu_group=None, prefix_len=None, max_prefix=0,
+                      blocks=None, out=None, ws=None):
+            self.calls.append((cu_q.tolist(), kv_len.tolist(), table.clone(), max_q, max_kv,
+                               None if cu_group is None else (cu_group.tolist(), prefix_len.tolist(), max_prefix), blocks))
+            out.zero_()
+            return out
+
+        def pick(q, bounds, cu_q, kv_len, table, max_q, max_kv, size, n, *, first, last, blocks, ws=None):
+            assert (size, n, first, last) == (page_size, *select)
+            blocks.zero_()
+            return blocks
+
+        monkeypatch.setattr(K.A, "fp8_linear", linear)
+        for name, f in (("paged_append", append), ("paged_attention", attention), ("select_blocks", pick)):
+            monkeypatch.setattr(K.P, name, f)
+        code = torch.zeros
+        self.b = K.PagedAttentionBlock(code((HQ + 2 * HKV) * D, HIDDEN), None, code(HIDDEN, HQ * D), None, HQ, HKV, D,
+                                       torch.zeros(max_len, D), max_seqs=max_seqs, max_len=max_len, max_tokens=max_tokens,
+                                       n_pages=n_pages, page_size=page_size, select=select)
+        self.b.cache.fill_(float("nan"))  # a slot that was never written
+        self.size = page_size
+        self.fed = [[] for _ in range(max_seqs)]
+        self.next = 1
+
+    def x(self, new):
+        """Tokens with the next numbers, noted per sequence."""
+        tokens = []
+        for s, n in enumerate(new):
+            for _ in range(n):
+                self.fed[s].append(self.next)
+                tokens.append(self.next)
+                self.next = self.next % 200 + 1  # numbers that bf16 holds
+        return torch.tensor(tokens).float()[:, None].expand(len(tokens), HIDDEN).bfloat16()
+
+    def read(self, table_row, n):
+        k = self.b.cache[:, :, 0, 0]
+        return [float(k[int(table_row[p // self.size]), p % self.size]) for p in range(n)]
+
+    def step(self, new, plan=None):
+        """Runs a plan and checks what its attention saw.  -> the plan"""
+        plan = plan or self.b.plan(new)
+        self.b.forward(self.x(new), plan)
+        cu, length, table, max_q, max_kv, group, blocks = self.calls[-1]
+        of = {}
+        if group:
+            bounds, prefix, most = group
+            for i, j, p in zip(bounds, bounds[1:], prefix):
+                assert p <= most and p % self.size == 0
+                for s in range(i, j):
+                    of[s] = (i, p)
+        for s, n in enumerate(new):
+            assert cu[s + 1] - cu[s] == n <= max_q
+            if not n:
+                continue
+            first, p = of.get(s, (s, 0))
+            assert length[s] == len(self.fed[s]) and length[s] - p <= max_kv
+            assert self.read(table[s], length[s]) == [float(t) for t in self.fed[s]]
+            assert self.read(table[first], p) == [float(t) for t in self.fed[s][:p]]
+        return plan
+
+    def check_pages(self):
+        """Every page is free or held, and counted once per sequence that holds it."""
+        held = [p for pages in self.b.pages for p in pages]
+        assert sorted(set(held) | set(self.b.free)) == list(range(self.b.n_pages)) and not set(held) & set(self.b.free)
+        assert len(set(self.b.free)) == len(self.b.free)
+        assert all(self.b.users[p] == held.count(p) for p in range(self.b.n_pages))
+        for s, pages in enumerate(self.b.pages):
+            assert self.b.table[s, :len(pages)].tolist() == pages and torch.all(self.b.table[s, len(pages):] == -1)
+
+    def fork(self, src, dst):
+        self.b.fork(src, dst)
+        self.fed[dst] = list(self.fed[src])
+        self.check_pages()
+
+
+def test_prompts_chunks_and_steps(monkeypatch):
+    m = Model(monkeypatch)
+    for new in ([40, 0, 7, 1], [3, 20, 0, 16], [1, 1, 1, 1], [0, 0, 30, 0]):
+        m.step(new)
+        m.check_pages()
+    assert [len(p) for p in m.b.pages] == [3, 2, 3, 2]
+
+
+def test_forks_share_what_is_full(monkeypatch):
+    m = Model(monkeypatch)
+    m.step([50])
+    m.fork(0, 2)
+    m.fork(2, 1)
+    assert m.b.pages[0][:3] == m.b.pages[1][:3] == m.b.pages[2][:3] and len({p[3] for p in m.b.pages[:3]}) == 3
+    m.step([1, 1, 1])
+    assert m.calls[-1][5] == ([0, 3], [48], 48)
+    m.step([3, 0, 20])  # an idle one between
+    assert m.calls[-1][5] == ([0, 3], [48], 48)
+    m.step([0, 1, 0, 5])
+    assert m.calls[-1][5] is None  # nobody shares with a neighbour that brings rows
+    m.step([0, 1, 1, 1])
+    assert m.calls[-1][5] == ([1, 3, 4], [48, 0], 48)
+    m.b.reset(0)
+    m.fed[0] = []
+    m.check_pages()
+    m.step([5, 1, 1])
+    m.b.reset()
+    assert sorted(m.b.free) == list(range(40)) and not any(m.b.users)
+
+
+def test_fork_at_a_page_end_and_of_nothing(monkeypatch):
+    m = Model(monkeypatch)
+    m.fork(0, 1)
+    assert m.b.pages[1] == []
+    m.step([32, 1])
+    m.fork(0, 3)
+    assert m.b.pages[3] == m.b.pages[0]
+    m.step([1, 0, 0, 1])
+    assert m.b.pages[3][:2] == m.b.pages[0][:2] and m.b.pages[3][2] != m.b.pages[0][2]
+
+
+def test_groups_join_while_they_share_enough(monkeypatch):
+    """A long shared prefix is not given up for a neighbour that shares little."""
+    m = Model(monkeypatch)
+    m.step([20])
+    m.fork(0, 3)          # shares one page with the others
+    m.step([140])
+    m.fork(0, 1)
+    m.fork(0, 2)          # shares ten
+    m.step([1, 1, 1, 1])
+    assert m.calls[-1][5] == ([0, 3, 4], [160, 0], 160)
+
+
+def test_advanced_plans_have_their_pages(monkeypatch):
+    m = Model(monkeypatch)
+    m.step([30, 15])
+    plan = m.b.plan([1, 1], max_kv=70)
+    assert [len(p) for p in m.b.pages[:2]] == [5, 4]  # 70 and 55 tokens
+    for i in range(40):
+        m.step([1, 1], plan)
+        if i < 39:
+            plan.advance()
+    m.check_pages()
+    assert [len(f) for f in m.fed[:2]] == [70, 55]
+    with pytest.raises(ValueError):
+        plan.advance()
+        m.b.forward(m.x([1, 1]), plan)
+
+
+def test_refusals(monkeypatch):
+    m = Model(monkeypatch, n_pages=6)
+    plan = m.step([60])
+    for bad in ((0, 0), (0, 4), (-1, 1), (4, 0)):
+        with pytest.raises(ValueError):
+            m.b.fork(*bad)
+    with pytest.raises(ValueError):
+        m.b.plan([0, 33])  # three pages, two are free
+    m.check_pages()
+    assert m.b.lens == [60, 0, 0, 0]
+    m.fork(0, 1)
+    m.step([0, 1])
+    with pytest.raises(ValueError):
+        m.b.fork(0, 1)  # holds tokens
+    late = m.b.plan([1])
+    with pytest.raises(ValueError):
+        m.b.fork(0, 2)  # a plan has not run
+    late.cancel()
+    m.b.reset(1)
+    m.step([0, 0, 32])
+    with pytest.raises(ValueError):
+        m.b.fork(0, 3)  # no page for the last one's copy
+    m.check_pages()
+    m.b.reset(0)
+    m.check_pages()
+    with pytest.raises(ValueError):
+        m.b.forward(m.x([60]), plan)
+    for kw in (dict(page_size=24), dict(n_pages=0), dict(select=(2, 1, 2)), dict(select=(4, 1, 0)), dict(select=(2000, 1, 1))):
+        with pytest.raises(ValueError):
+            Model(monkeypatch, **kw)
+
+
+def test_selection_is_for_single_tokens(monkeypatch):
+    m = Model(monkeypatch, select=(4, 1, 2))
+    m.step([100, 30])
+    assert m.calls[-1][6] is None
+    m.step([1, 1])
+    assert m.calls[-1][6].shape == (2, HKV, 4)
+    m.step([2, 1])
+    assert m.calls[-1][6] is None
+    m.fork(0, 2)
+    m.step([1, 0, 1])
+    assert m.calls[-1][6] is not None and m.calls[-1][5] is None
+
+
+def test_empty_plan(monkeypatch):
+    m = Model(monkeypatch)
+    plan = m.b.plan([])
+    assert m.b.forward(torch.zeros(0, HIDDEN).bfloat16(), plan).shape == (0, HIDDEN)
+    m.check_pages()
