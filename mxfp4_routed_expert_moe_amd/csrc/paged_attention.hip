@@ -781,7 +781,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(Paged
     if (key + kKeysP < kend) {
       next = to_spots(a, after);
       issue(to, next);
-      after = find_all(min(key + 2 * kKeysP, kend - 1 & ~(kKeysP - 1)));
+      after = find_all(key + 2 * kKeysP);  // past the end: some page, unused
     }
     __builtin_amdgcn_sched_barrier(0);
   };

@@ -106,16 +106,26 @@ def _pages(t, name, dev, shape=None):
         raise ValueError(f"{name} must have four dimensions (pages, page_size, heads, head_dim)")
     if shape is not None and have != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(have)}")
-    pages, _, heads, d = have
     page, row, head, one = t.stride()
-    if one != 1 and d > 1:
+    if one != 1 and have[3] > 1:
         raise ValueError(f"{name} must have unit stride inside a head")
     # a dimension of one entry may carry any stride
-    if heads <= 1:
-        head = max(d, 8)
-    if pages <= 1:
+    if have[2] <= 1:
+        head = max(have[3], 8)
+    if have[0] <= 1:
         page = max(page, 8) // 8 * 8
     return t.data_ptr(), page, row, head
+
+
+def _vector(t, dtypes, name, dev, n):
+    """The address of a contiguous vector of n elements (None: 0)."""
+    if t is None:
+        return 0
+    if t.dtype not in dtypes or t.get_device() != dev:
+        _refuse(t, dtypes, name, dev)
+    if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape ({n},), got {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _seqs(cu_q, kv_len, page_table, dev):
@@ -123,17 +133,18 @@ def _seqs(cu_q, kv_len, page_table, dev):
     if cu_q.dim() != 1 or cu_q.numel() < 1:
         raise ValueError("cu_q must be [n_seqs + 1]")
     n = cu_q.numel() - 1
-    cu = _flat(cu_q, _I32, "cu_q", dev)
-    length = _flat(kv_len, _I32, "kv_len", dev, (n,))
     if page_table.dtype not in _I32 or page_table.get_device() != dev:
         _refuse(page_table, _I32, "page_table", dev)
-    if page_table.dim() != 2 or page_table.shape[0] != n:
+    if page_table.dim() != 2:
         raise ValueError(f"page_table must be [{n}, pages], got {tuple(page_table.shape)}")
-    width = page_table.shape[1]
+    rows, width = page_table.shape
+    if rows != n:
+        raise ValueError(f"page_table must be [{n}, pages], got {(rows, width)}")
     row, one = page_table.stride()
     if one != 1 and width > 1:
         raise ValueError("page_table must have unit stride along its rows")
-    return n, width, row if n > 1 else width, cu, length, page_table.data_ptr()
+    return (n, width, row if n > 1 else width, _flat(cu_q, _I32, "cu_q", dev), _vector(kv_len, _I32, "kv_len", dev, n),
+            page_table.data_ptr())
 
 
 # ---------------------------------------------------------------- append
@@ -169,15 +180,9 @@ def paged_append(k, v, k_pages, v_pages, cu_q, kv_len, page_table, *, q=None, q_
         hqo = _heads(q_out, "q_out", dev, qshape)
     elif q_out is not None or q_weight is not None:
         raise ValueError("q_out and q_weight need q")
-    bp = qw = kw = pos = cs = P = R = 0
+    bp = cs = P = R = 0
     if bounds is not None:
         bp = _flat(bounds, _BF16, "bounds", dev, (pshape[0], 2, Hk, D))
-    if q_weight is not None:
-        qw = _flat(q_weight, _F32, "q_weight", dev, (D,))
-    if k_weight is not None:
-        kw = _flat(k_weight, _F32, "k_weight", dev, (D,))
-    if positions is not None:
-        pos = _flat(positions, _I32, "positions", dev, (T,))
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [n_positions, rot_dim]")
@@ -185,7 +190,8 @@ def paged_append(k, v, k_pages, v_pages, cu_q, kv_len, page_table, *, q=None, q_
         cs = _flat(cos_sin, _F32, "cos_sin", dev)
     a = _APPEND.pack(B.MOE_ABI_VERSION, D, Hq, Hk, n, T, pshape[0], pshape[1], width, 0, stride, cu, length, table,
                      1 if norm else 0, eps, P, R, rot_offset, 1 if interleaved else 0, *hq, *hqo, *hk, *hv, *pk, *pv,
-                     bp, qw, kw, pos, cs)
+                     bp, _vector(q_weight, _F32, "q_weight", dev, D), _vector(k_weight, _F32, "k_weight", dev, D),
+                     _vector(positions, _I32, "positions", dev, T), cs)
     st = lib().moe_paged_append(a, _stream(dev))
     if st:
         raise MoeError("moe_paged_append", st)
@@ -236,8 +242,8 @@ def paged_attention(q, k_pages, v_pages, cu_q, kv_len, page_table, max_q: int, m
     groups = n_blocks = gp = pp = bp = lp = 0
     if cu_group is not None and prefix_len is not None:
         groups = prefix_len.numel()
-        gp = _flat(cu_group, _I32, "cu_group", dev, (groups + 1,))
-        pp = _flat(prefix_len, _I32, "prefix_len", dev, (groups,))
+        gp = _vector(cu_group, _I32, "cu_group", dev, groups + 1)
+        pp = _vector(prefix_len, _I32, "prefix_len", dev, groups)
     elif cu_group is not None or prefix_len is not None:
         raise ValueError("cu_group and prefix_len go together")
     if blocks is not None:

@@ -297,7 +297,10 @@ GROUPS = [
     ([1] * 6, [90] * 6, [1, 1, 3, 4, 5], [80, 64, 0, 15], 4, 2, 128, 16),
     # a prefix that rows see part of (they are rows of it), or that is longer than the sequence
     ([60, 60], [100, 100], [0, 2], [96], 4, 2, 64, 16), ([3, 1], [50, 20], [0, 2], [48], 2, 2, 128, 16),
-    ([1] * 40, [600 + 7 * i for i in range(40)], [0, 40], [576], 8, 2, 64, 64)]
+    ([1] * 40, [600 + 7 * i for i in range(40)], [0, 40], [576], 8, 2, 64, 64),
+    # own keys that begin inside a tile of 64, and end in its first, second and last 16
+    ([1, 1, 1], [230, 195, 300], [0, 3], [106], 2, 1, 64, 16), ([9, 40], [300, 470], [0, 2], [250], 4, 2, 128, 16),
+    ([2, 70], [330, 305], [0, 2], [165], 2, 1, 256, 32), ([0, 3], [190, 230], [0, 2], [106], 2, 1, 256, 16)]
 
 
 @pytest.mark.parametrize("lq,lk,cu,prefix,Hq,Hkv,D,page", GROUPS)
@@ -774,3 +777,83 @@ def test_no_tokens():
         assert torch.all(pool == 0)
         blocks = P.select_blocks(q, z(pool.shape[0], 2, 1, 64), cu, n, table, 3, min(3, width), 16, 2)
         assert torch.all(blocks == -1)
+
+
+# ---------------------------------------------------------------- many, odd, strided
+def test_many_sequences_and_groups():
+    """More sequences and groups than a wave looks up at once, in a table whose rows are parts of wider ones; sequences of no rows
+    and of no tokens among them."""
+    _say("many sequences")
+    g = np.random.default_rng(15)
+    B, page, Hq, Hkv, D = 200, 16, 4, 2, 64
+    lq = [int(n) for n in g.integers(0, 4, B)]
+    lq[7], lq[150] = 45, 70
+    lk = [n + int(g.integers(0, 90)) for n in lq]
+    lk[3], lk[20], lk[199] = 0, 0, 300
+    cu = np.unique(np.r_[0, g.integers(0, B, 90), B])
+    prefix = [int(min(lk[b] for b in range(i, j))) - 5 for i, j in zip(cu, cu[1:])]
+    table, n_pages = _group_table(g, lk, page, cu, prefix)
+    wide = torch.full((B, table.shape[1] + 9), 77777, dtype=torch.int32, device="cuda")
+    wide[:, 4:4 + table.shape[1]] = _i32(table)
+    strided = wide[:, 4:4 + table.shape[1]]
+    seqs, T = _seqs(lq, lk), sum(lq)
+    kp, vp, kt, vt = _pool(g, n_pages, page, Hkv, D)
+    q = AR.bf16(g.normal(0, 1, (T, Hq, D)))
+    see = PR.visible(seqs, table, page, n_pages, Hkv)
+    at = _i32(np.r_[0, np.cumsum(lq)]), _i32(lk), strided
+    out = P.paged_attention(_bf16(q), kt, vt, *at, max(lq), max(lk))
+    _check(out, None, q, kp, vp, table, seqs, see, D ** -0.5)
+    out = P.paged_attention(_bf16(q), kt, vt, *at, max(lq), max(lk), cu_group=_i32(cu), prefix_len=_i32(prefix), max_prefix=max(prefix))
+    _check(out, None, q, kp, vp, table, seqs, see, D ** -0.5)
+    bounds = torch.stack([kt.amin(1), kt.amax(1)], 1).contiguous()
+    blocks = P.select_blocks(_bf16(q), bounds, *at, max(lq), max(lk), page, 3, first=0)
+    want = PR.select(q, _np(bounds), table, seqs, page, 3, 0, 1)
+    assert np.array_equal(blocks.cpu().numpy(), want)
+    out = P.paged_attention(_bf16(q), kt, vt, *at, max(lq), max(lk), blocks=blocks)
+    _check(out, None, q, kp, vp, table, seqs, PR.visible(seqs, table, page, n_pages, Hkv, want), D ** -0.5)
+    k, v = (AR.bf16(g.normal(0, 1, (T, Hkv, D))) for _ in range(2))
+    own, n_own = _table(g, lk, page)  # every sequence writes to pages of its own
+    kt, vt = (torch.zeros(n_own, page, Hkv, D, dtype=BF, device="cuda") for _ in range(2))
+    P.paged_append(_bf16(k), _bf16(v), kt, vt, at[0], at[1], _i32(own), norm=False)
+    got_k, got_v = _np(kt), _np(vt)
+    count = 0
+    for b, (q0, n, m) in enumerate(seqs):
+        for i in range(n):
+            p = i + m - n
+            if p >= 0:
+                at_ = own[b, p // page], p % page
+                assert np.array_equal(got_k[at_], k[q0 + i]) and np.array_equal(got_v[at_], v[q0 + i])
+                count += 1
+    assert np.count_nonzero(np.any(got_k != 0, (2, 3))) == count
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_shapes(seed):
+    """Shapes drawn over everything that the operators take."""
+    g = np.random.default_rng(1000 + seed)
+    D, page, Hkv = int(g.choice([64, 128, 256])), int(g.choice([16, 32, 64, 128])), int(g.choice([1, 2, 3, 4]))
+    Hq = Hkv * int(g.choice([1, 2, 3, 4, 5, 7, 8, 16, 33]))
+    B = int(g.integers(1, 7))
+    lq = [int(n) for n in (np.ones(B, int) if seed % 3 == 0 else g.integers(0, 4 + 70 * (seed % 2), B))]
+    lk = [n + int(g.integers(0, 500)) if g.random() < 0.9 else int(g.integers(0, n + 1)) for n in lq]
+    _say("random", seed, D, page, Hq, Hkv, lq, lk)
+    cu = np.unique(np.r_[0, g.integers(0, B + 1, 2), B])
+    prefix = [int(g.integers(-3, 1 + max(min(lk[b] for b in range(i, j)), 0) + 1)) for i, j in zip(cu, cu[1:])]
+    table, n_pages = _group_table(g, lk, page, cu, prefix)
+    kp, vp, kt, vt = _pool(g, n_pages, page, Hkv, D, layout=("pshd", "phsd", "both")[seed % 3])
+    seqs = _seqs(lq, lk)
+    q = AR.bf16(g.normal(0, 1.5, (sum(lq), Hq, D)))
+    see = PR.visible(seqs, table, page, n_pages, Hkv)
+    for kw in ({}, dict(cu_group=_i32(cu), prefix_len=_i32(prefix), max_prefix=max(max(prefix), 0))):
+        out, lse = _run(_bf16(q), kt, vt, table, seqs, **kw)
+        _check(out, lse, q, kp, vp, table, seqs, see, D ** -0.5)
+    n = int(g.integers(1, 12))
+    last = int(g.integers(1, n + 1))
+    first = int(g.integers(0, n - last + 1))
+    bounds = torch.stack([kt.amin(1), kt.amax(1)], 1).contiguous()
+    blocks = P.select_blocks(_bf16(q), bounds, _i32(np.r_[0, np.cumsum(lq)]), _i32(lk), _i32(table), max(lq), max(lk), page, n,
+                             first=first, last=last)
+    want = PR.select(q, _np(bounds), table, seqs, page, n, first, last)
+    assert np.array_equal(blocks.cpu().numpy(), want)
+    out, lse = _run(_bf16(q), kt, vt, table, seqs, blocks=blocks)
+    _check(out, lse, q, kp, vp, table, seqs, PR.visible(seqs, table, page, n_pages, Hkv, want), D ** -0.5)
