@@ -122,9 +122,10 @@ __device__ __forceinline__ Sides query_sides(const uint16_t* q, int64_t head_str
     unpack8(ld16(q + g * head_stride), x);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {  // NaN goes up
+      const double d = static_cast<double>(x[j]);
       const bool below = x[j] < 0.f;
-      s.up[j] += static_cast<double>(below ? 0.f : x[j]);
-      s.down[j] += static_cast<double>(below ? x[j] : 0.f);
+      s.up[j] += below ? 0.0 : d;
+      s.down[j] += below ? d : 0.0;
     }
   }
   return s;
@@ -308,7 +309,7 @@ __device__ __forceinline__ int32_t* out_row(const SelectArgs& a, int row, int he
 constexpr int kFusedThreads = 512;
 
 template <int L, int PER>
-__global__ __launch_bounds__(kFusedThreads, 4) void token_kernel(SelectArgs a) {
+__global__ __launch_bounds__(kFusedThreads, 2) void token_kernel(SelectArgs a) {
   __shared__ uint64_t s_key[64 * PER];
   const int head = blockIdx.x % a.kv_heads, row = blockIdx.x / a.kv_heads;
   const RowWork w = find_row(a, row);
@@ -506,12 +507,19 @@ inline int score_stride(const moe_select& d) {
   const int pages = (d.max_kv + d.p.page_size - 1) / d.p.page_size;
   return std::max((pages + 7) / 8 * 8, 8);
 }
-// How the scores are made, from the shape fields, as the workspace.
+// How the scores are made, from the shape fields, as the workspace.  32 query heads of 128 over
+// 8, pages of 64 (us: one block a token and head; several and the workspace; tiles):
+//   64 rows of one sequence, 512 pages 23.4, 26.4, 23.1; 128 rows 40.3, 42.7, 24.1; four sequences of
+//   32 rows 26.9, 33.8, 34.1, of 64 rows 47.3, 57.5, 35.2; 16 heads of 64 over 2, 256 pages, 128 rows 10.6,
+//   12.6, 16.8, 512 rows 26.8, 24.7, 17.9: tiles from 64 rows a sequence and 512 rows x heads on;
+//   single tokens, 4 of 256 pages 10.1, 10.6; 4 of 512 13.1, 10.9; 16 of 512 14.9, 15.0; 16 of 1024 26.6, 23.1;
+//   64 of 1024 46.8, 57.4; 16 of 2048 38.8, 34.9; 64 of 2048 77.4, 106.6: several blocks each where
+//   there are fewer rows x heads than a quarter of the pages, and more than 256 of those.
 inline Way pick_way(const moe_select& d) {
-  if (d.max_q >= 4 && d.p.q_rows >= 4 * static_cast<int64_t>(d.p.n_seqs)) return kTiles;
-  const int pages = score_stride(d);
   const int64_t items = static_cast<int64_t>(d.p.q_rows) * d.p.kv_heads;
-  return pages <= 512 || (pages <= 2048 && items >= 64) ? kTokenBlock : kTokenSplit;
+  if (d.max_q >= 64 && d.p.q_rows >= 64 * static_cast<int64_t>(d.p.n_seqs) && items >= 512) return kTiles;
+  const int pages = score_stride(d);
+  return pages <= 256 || (pages <= 2048 && items >= pages / 4) ? kTokenBlock : kTokenSplit;
 }
 // Rows of a launch: their scores fit kBatchBytes, and the grid 65535 blocks along y; whole tiles.
 inline int batch_rows(const moe_select& d) {

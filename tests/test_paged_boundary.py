@@ -160,7 +160,7 @@ def test_select_checks():
     assert _select(table_pages=32769, table_stride=32769, page_size=16, max_kv=32769 * 16) == ESHAPE
     assert _select(q=_heads(base=None)) == EINVAL and _select(q=_heads(row=4)) == EALIGN
     assert _select(q_rows=B.MOE_MAX_TOKENS, kv_heads=128, q_heads=128) == ESHAPE and _select(bounds=FAKE + 8) == EALIGN
-    for long in (dict(table_pages=3000, table_stride=3000, max_kv=192000), dict(max_q=40, n_seqs=1)):
+    for long in (dict(table_pages=3000, table_stride=3000, max_kv=192000), dict(q_rows=256, max_q=256, n_seqs=1)):
         need = P.lib().moe_select_blocks_workspace_size(ctypes.byref(_select_desc(**long)))
         assert need > 0 and _select(ws_bytes=need - 1, **long) == EWORKSPACE
         assert _select(ws=FAKE + 8, **long) == EALIGN and _select(ws=None, **long) == EINVAL

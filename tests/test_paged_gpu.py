@@ -533,7 +533,10 @@ SELECT = [
     ([1, 1], [9000, 700], 16, 2, 256, 32, 17, 0, 1), ([40, 0, 3], [900, 5, 33], 6, 2, 128, 16, 8, 2, 3),
     ([20], [5], 4, 2, 64, 16, 3, 1, 1), ([130], [4000], 5, 1, 128, 64, 12, 1, 2), ([7], [70000], 8, 4, 64, 16, 64, 1, 1),
     ([2], [150000], 2, 1, 64, 16, 200, 3, 4), ([1], [524288], 2, 2, 64, 16, 1024, 1, 1), ([3], [600], 4, 4, 128, 16, 38, 1, 1),
-    ([17, 16, 15, 1], [1700, 1600, 1500, 1400], 32, 4, 128, 16, 9, 1, 2), ([65], [40000], 4, 2, 256, 128, 20, 0, 1)]
+    ([17, 16, 15, 1], [1700, 1600, 1500, 1400], 32, 4, 128, 16, 9, 1, 2), ([65], [40000], 4, 2, 256, 128, 20, 0, 1),
+    # tiles of 16 rows: with ends of sequences and empty ones inside, rows that see fewer blocks than are wanted, every head size
+    ([300, 0, 5, 211], [700, 0, 5, 1900], 4, 2, 128, 16, 9, 1, 2), ([600], [600], 2, 1, 64, 16, 7, 0, 1), ([100, 90, 110], [900, 90, 4000], 9, 3, 256, 32, 12, 2, 3),
+    ([260], [9000], 4, 2, 64, 16, 30, 1, 1)]
 
 
 @pytest.mark.parametrize("lq,lk,Hq,Hkv,D,page,n,first,last", SELECT)
@@ -593,6 +596,23 @@ def test_select_in_batches():
     for r in rows:
         want = PR.select(q[r:r + 1], bounds, table, [(0, 1, L - T + 1 + r)], page, 10, 1, 1)
         assert np.array_equal(got[r], want[0]), r
+
+
+def test_select_single_tokens_in_batches():
+    """The same for single tokens of many sequences over very long tables."""
+    B, page, Hkv, D, n_pages = 600, 16, 2, 64, 900
+    width = 32768
+    _say("select batches of tokens")
+    g = np.random.default_rng(10)
+    table = torch.randint(0, n_pages, (B, width), dtype=torch.int32, device="cuda")
+    lk = g.integers(1, width * page + 1, B)
+    lk[0], lk[599] = width * page, width * page - 3
+    bounds = AR.bf16(np.sort(g.normal(0, 1, (n_pages, 2, Hkv, D)), 1))
+    q = AR.bf16(g.normal(0, 1, (B, 2, D)))
+    got = P.select_blocks(_bf16(q), _bf16(bounds), _i32(np.arange(B + 1)), _i32(lk), table, 1, width * page, page, 40,
+                          first=2).cpu().numpy()
+    for r in (0, 255, 511, 512, 598, 599):  # a table of 900 pages: equal scores everywhere
+        assert np.array_equal(got[r], PR.select(q[r:r + 1], bounds, table[r:r + 1].cpu().numpy(), [(0, 1, int(lk[r]))], page, 40, 2, 1)[0]), r
 
 
 # ---------------------------------------------------------------- together
