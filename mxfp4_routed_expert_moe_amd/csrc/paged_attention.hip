@@ -6,14 +6,19 @@
 // fills at most 16 rows of a tile, and a page holds a multiple of 16 keys, so every
 // instruction has one page and the tile's keys need one lookup per 16 ("half" below: 16 keys).
 //
-// Three kernels write shares of rows, a fourth joins them:
+// Two kernels write shares of rows, a third joins them:
 //  token  32 rows of a sequence (its new tokens' heads, few of them), the waves split
 //         the keys; the sequence's own keys, or those of listed blocks
-//  rows   128 rows of a sequence over its own keys, or of a whole group over
-//         the prefix that its sequences share
+//  rows   128 rows of a sequence over its own keys, or over listed blocks; in the same launch
+//         128 rows of a whole group over the prefix that its sequences share
 // With a shared prefix a row has shares of both: slots 0 .. prefix_splits - 1 are the
 // prefix's, the others the sequence's own.  Every slot of a row is written, if only
 // with a sum of 0, so the join needs to know nothing about groups or lists.
+//
+// A sequence alone costs what it does over a contiguous cache (us, pages of 64; contiguous): 64 tokens over up to
+// 8192 keys 216, 212; 4 over 1024 10.8, 10.6; one over 65536 57, 57; a prompt of 4096 152, 151; with pages of 16,
+// a lookup per 16 keys, 219 and 147.  Heads of 256 lose more, 25 and 22 for one token over 32768 keys, 202 and 177 for
+// a prompt of 4096: all registers are in use, and the addresses are made anew for every tile.
 #include <math.h>
 
 #include <algorithm>
@@ -175,7 +180,7 @@ __device__ __forceinline__ void empty_share(const PagedArgs& a, int slot, int64_
   a.part_ml[part_row(a, slot, q_row, head)] = make_float2(kNegInf, 0.f);
 }
 
-// Heads of 256 leave no registers for the addresses.
+// Heads of 256 leave no registers for the LDS addresses (kept, the loops spilled).
 template <int D>
 constexpr bool kKeep = D < 256;
 
@@ -402,6 +407,11 @@ enum Keys {
   kListSeveral // listed blocks, tiles of several tokens, which see different blocks
 };
 
+// A block per sequence, key head and split; each wave takes every NW-th tile of 32 keys through two stages of
+// its own, so no wave waits for another before the merge.  Bound by HBM where there are many keys (32 tokens over 64
+// of 512 pages each, 494 MB: 93 us, 5.3 TB/s), by the latency of a list, a tile and the join where there are few (4
+// tokens, 16 pages each: 12.7 us).  A tile's pages are looked up one tile before its loads go out: looked up with them, every
+// tile waited for the table (4 tokens over 1024 keys 13.3 against 12.9).
 // N: spots of a tile, 1 where a page holds whole tiles.
 template <int D, Keys KEYS, int NW, int N>
 __global__ __launch_bounds__(64 * NW, 1) void paged_token_kernel(PagedArgs a) {
@@ -627,6 +637,11 @@ __global__ __launch_bounds__(64 * NW, 1) void paged_token_kernel(PagedArgs a) {
 constexpr int kRowsP = 128;  // rows of a block: 4 waves x 32
 constexpr int kKeysP = 64;   // keys of a tile
 
+// 4 waves x 32 rows and tiles of 64 keys that all of them read: 2 x 32 KB of LDS at heads of 128, two blocks on a
+// CU, one's softmax under the other's products.  A prefix of 16384 keys under 1100 rows of 32 heads: 300 us for the
+// whole call, 0.92 PFLOP/s (matrix pipes busy 49 %, vector pipes 41 %).  Listed blocks are masked
+// tiles throughout, as neighbouring tokens list most pages together but not all (509 tokens, 40 pages of 32 each: 48 us; in
+// 32-row tiles 94).
 // A launch has units of kv_heads blocks each: (tile, split) pairs of sequences over their
 // own keys, or over listed blocks, and behind them those of groups over their prefixes.
 // (64 single tokens behind a prefix of 16384, whole call: 101 us; prefix first 113; the kinds evenly mixed 113 to
@@ -888,7 +903,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(Paged
 // ---------------------------------------------------------------- the join of the shares
 // A thread per four outputs of a row, kJoin shares at a time, so that their latencies
 // overlap; with more than kJoinShared slots the block has one row, and its thread groups
-// take turns over them and meet in LDS.  Either way in a fixed order.
+// take turns over them and meet in LDS.  Either way in a fixed order.  (64 tokens of 32 heads in 18 slots, 19 MB: @ us.)
 constexpr int kJoin = 8, kJoinShared = 2 * kJoin;
 template <int D>
 __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a) {
@@ -1017,6 +1032,8 @@ int64_t pick_chunk(int64_t keys, int64_t tiles, int64_t unit, int64_t want, int6
 // Tiles of kRowsP rows that `rows` rows in up to `parts` sequences or groups make.
 int64_t tile_bound(int64_t rows, int64_t parts) { return (rows + (kRowsP - 1) * parts) / kRowsP; }
 
+// Measured in us as a HIP graph, heads of 128 unless said; want, least and most are blocks, and keys of a block, in the
+// terms of pick_chunk.
 Plan make_plan(const moe_paged_attn& d) {
   Plan p = {};
   const moe_paged& s = d.p;
@@ -1024,21 +1041,36 @@ Plan make_plan(const moe_paged_attn& d) {
   const int64_t seqs = std::min<int64_t>(s.n_seqs, s.q_rows);
   const bool listed = d.n_blocks > 0, grouped = d.n_groups > 0;
   const bool few = d.max_q * g <= kRowsT;
+  // One launch for prefixes and own keys, so that neither waits for the other's last blocks: the rows
+  // kernel takes both, also for single tokens (64 tokens behind 16384 keys 114 in two launches, 105).
   p.token = few && !grouped;
   p.tiles = p.token ? s.n_seqs : tile_bound(s.q_rows * g, seqs);
   const int64_t tiles = std::max<int64_t>(p.tiles * s.kv_heads, 1);
-  int64_t keys = std::max(d.max_kv, 1);
-  if (grouped) keys += s.page_size - 1;  // what is left of the prefix's last page
+  const int64_t rest = grouped ? s.page_size - 1 : 0;  // of the prefix's last page
+  int64_t keys = std::max(d.max_kv, 1) + rest;
   if (listed)
     keys = std::max<int64_t>(1, std::min<int64_t>(static_cast<int64_t>(tile_tokens(g, d.max_q, p.token)) * d.n_blocks,
                                                   ceil_div(keys, s.page_size))) * s.page_size;
+  // Two waves where there are many tiles: two blocks share a CU, and one loads while the other merges (64
+  // tokens over up to 1024 keys 39 against 42 with four, over 8192 216 and 218); four where there are few (16
+  // over 4096, heads of 64: 21 against 24).  Heads of 256 have LDS for two.
   p.waves = s.head_dim == 256 || tiles >= 2 * kCus ? 2 : 4;
   const int64_t unit = p.token ? kKeysT * p.waves : kKeysP;
-  const int64_t want = s.head_dim > (p.token ? 64 : 128) ? kCus : 2 * kCus;
+  // As many blocks as the card holds at a time; half as many beside a prefix, whose own
+  // fill the card too (three chunks of 200 behind 8192, heads of 256: 147 against 150; heads of 128 the same).  Listed
+  // blocks of 509 tokens: half of them 54, twice 48, as they are 48.
+  const int64_t want = (s.head_dim > (p.token ? 64 : 128) ? kCus : 2 * kCus) / (grouped ? 2 : 1);
+  // Pieces of at least two or four tiles a wave (one listed token over 64 pages: 12.6 with one, 14 with two, 14.4 with
+  // four, 18 with eight; 4 tokens behind a prefix 13.7, 12.9, 12.9), more in the rows kernel the more tiles
+  // there are (listed blocks of 509 tokens: four 56, eight 47, sixteen 50).
   const int64_t least = p.token ? (keys <= 4 * unit ? 4 : 2) * unit
                                 : std::min(std::max(tiles / 16, int64_t{4}), int64_t{16}) * unit;
+  // Few rows over long caches of many lengths: at most 16 units a piece, so that a long one does not run on
+  // alone, but no more than kRounds rounds of blocks.  8, 16, 32: 64 tokens over 8192 keys 221, 216, 223; behind a
+  // prefix 24 over 8192 -, 110, 116, heads of 64, 64 over 4096 -, 75, 81.  What is left of the prefix's page
+  // makes no piece of its own (64 over 2048 104 with it, 99; 24 over 8192 110, 103; 64 over 4096, heads of 256, 168, 178).
   const int64_t most = !few || listed ? INT32_MAX
-                                      : std::max(16 * unit, ceil_div(keys, std::max(kRounds * kCus / tiles, int64_t{1})));
+                                      : std::max(16 * unit + rest, ceil_div(keys, std::max(kRounds * kCus / tiles, int64_t{1})));
   const int64_t chunk = pick_chunk(keys, tiles, unit, want, least, most);
   if (listed) {
     // How many blocks a tile's tokens list together is known to the kernel alone: as many as one
@@ -1048,19 +1080,20 @@ Plan make_plan(const moe_paged_attn& d) {
     p.chunk = static_cast<int>(least_blocks);
     p.splits = static_cast<int>(std::max(wanted, ceil_div(keys / s.page_size, kList)));
   } else {
-    p.chunk = static_cast<int>(std::min<int64_t>(chunk, 1 << 30));
+    p.chunk = static_cast<int>(chunk);
     p.splits = static_cast<int>(ceil_div(keys, chunk));
   }
   if (grouped && d.max_prefix >= s.page_size) {
     p.prefix_tiles = tile_bound(s.q_rows * g, std::min<int64_t>(d.n_groups, s.q_rows));
-    const int64_t blocks = p.prefix_tiles * s.kv_heads, row_bytes = int64_t{8} * s.q_rows * s.q_heads * s.head_dim;
-    int64_t fill = kCus;
-    if (s.head_dim <= 128) {
-      const int64_t splits = std::max<int64_t>(kCus / std::max<int64_t>(blocks, 1), 1), steps = blocks * ceil_div(d.max_prefix, kKeysP);
-      if (steps / kCus * 400 > splits * row_bytes / 5000) fill = 2 * kCus;
-    }
-    const int64_t piece = pick_chunk(d.max_prefix, blocks, kKeysP, fill,
-                                     std::min(std::max(blocks / 16, int64_t{4}), int64_t{16}) * kKeysP, 1 << 30);
+    const int64_t blocks = p.prefix_tiles * s.kv_heads;
+    // One block a CU, or two where that gains more than the shares of twice the splits cost: a second block on a CU
+    // hides about a third of a tile's 400 ns (heads of 256, which have a CU each: its smaller pieces leave less at the end).  256
+    // blocks, 512: eight chunks of up to 256 behind 16384 432, 295; four of 64 behind 8192 44, 48; heads of 256, three of 200 164, 150.
+    const int64_t splits = std::max<int64_t>(kCus / std::max<int64_t>(blocks, 1), 1);
+    const int64_t gain = blocks * ceil_div(d.max_prefix, kKeysP) / kCus * (s.head_dim == 256 ? 800 : s.head_dim);
+    const int64_t cost = splits * 8 * s.q_rows * s.q_heads * s.head_dim / 5000;  // ns: stored and loaded once at 5 TB/s
+    const int64_t piece = pick_chunk(d.max_prefix, blocks, kKeysP, gain > cost ? 2 * kCus : kCus,
+                                     std::min(std::max(blocks / 16, int64_t{4}), int64_t{16}) * kKeysP, INT32_MAX);
     p.prefix_chunk = static_cast<int>(piece);
     p.prefix_splits = static_cast<int>(ceil_div(d.max_prefix, piece));
   }

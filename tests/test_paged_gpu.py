@@ -774,9 +774,14 @@ def test_binding_refusals():
                      ((q, bounds, cu, n, table, 4, 4, 16, 2), dict(blocks=_i32(np.zeros((4, 1, 3)))))]:
         with pytest.raises(ValueError):
             P.select_blocks(*args, **kw)
-    for kw in (dict(first=2), dict(last=0), dict(ws=torch.zeros(8, dtype=torch.uint8, device="cuda"))):
+    for kw in (dict(first=2), dict(last=0)):
         with pytest.raises(P.MoeError):
             P.select_blocks(q, bounds, cu, n, table, 4, 4, 16, 2, **kw)
+    # 4 rows over 512 pages: the scores go through a workspace
+    long, ws = _i32(np.zeros((1, 512))), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    assert P.select_blocks_workspace(q, bounds, 1, 4, 8192, 16).numel() > 256
+    with pytest.raises(P.MoeError):
+        P.select_blocks(q, bounds, cu, n, long, 4, 8192, 16, 2, ws=ws)
 
 
 def test_no_tokens():
