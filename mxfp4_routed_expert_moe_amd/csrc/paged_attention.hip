@@ -638,8 +638,8 @@ constexpr int kRowsP = 128;  // rows of a block: 4 waves x 32
 constexpr int kKeysP = 64;   // keys of a tile
 
 // 4 waves x 32 rows and tiles of 64 keys that all of them read: 2 x 32 KB of LDS at heads of 128, two blocks on a
-// CU, one's softmax under the other's products.  A prefix of 16384 keys under 1100 rows of 32 heads: 300 us for the
-// whole call, 0.92 PFLOP/s (matrix pipes busy 49 %, vector pipes 41 %).  Listed blocks are masked
+// CU, one's softmax under the other's products.  A prefix of 16384 keys under 1100 rows of 32 heads: 296 us for the
+// whole call, 0.92 PFLOP/s (matrix pipes busy 45 %, vector pipes 41 %).  Listed blocks are masked
 // tiles throughout, as neighbouring tokens list most pages together but not all (509 tokens, 40 pages of 32 each: 48 us; in
 // 32-row tiles 94).
 // A launch has units of kv_heads blocks each: (tile, split) pairs of sequences over their
@@ -903,7 +903,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(Paged
 // ---------------------------------------------------------------- the join of the shares
 // A thread per four outputs of a row, kJoin shares at a time, so that their latencies
 // overlap; with more than kJoinShared slots the block has one row, and its thread groups
-// take turns over them and meet in LDS.  Either way in a fixed order.  (64 tokens of 32 heads in 18 slots, 19 MB: @ us.)
+// take turns over them and meet in LDS.  Either way in a fixed order.  (64 tokens of 32 heads in 18 slots, 19 MB: 9 us.)
 constexpr int kJoin = 8, kJoinShared = 2 * kJoin;
 template <int D>
 __global__ __launch_bounds__(256) void paged_join_kernel(PagedArgs a) {

@@ -306,6 +306,9 @@ __device__ __forceinline__ int32_t* out_row(const SelectArgs& a, int row, int he
 }
 
 // ---------------------------------------------------------------- a token in a block
+// Bound by the vector unit: eight columns of a page are 8 conversions and 8 FMAs of float64 for each bound.  64 tokens of
+// 32 heads of 128 over 8, 512 pages of 64: 24 us for 67 MB (13 at the copy rate), vector pipes busy half of the
+// time; scored by several blocks and chosen by a second launch 26.
 constexpr int kFusedThreads = 512;
 
 template <int L, int PER>
@@ -346,6 +349,8 @@ __global__ __launch_bounds__(256) void score_kernel(SelectArgs a) {
 // l / 16 at a time, and gets rows l / 16 + 4 r of page l % 16.  The order of the columns is free: lane l
 // takes eight neighbouring ones, 32 c + 8 (l / 16) + e, as they are loaded.  Q+ and Q- of
 // the rows are made once by the block and kept in LDS; the waves take 16 pages in turn.
+// 1021 tokens of 16 heads of 128 over 2, 1024 pages: 40 us with the choice, 16 at the rate of a large float64
+// product (28 for the scores, matrix pipes busy 38 %, making Q+ and Q- is 12 of them; 12 for the choice); one token at a time 281.
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 constexpr int kTileRows = 16, kTilePages = 256;
 
@@ -438,7 +443,7 @@ __global__ __launch_bounds__(256) void tile_kernel(SelectArgs a) {
 
 // ---------------------------------------------------------------- choice from the workspace
 // WAVES waves hold 64 * PER scores each, wave w those from 64 * PER * w on.  Where a token
-// and head has one wave, four of them stand in a workgroup.
+// and head has one wave, four of them stand in a workgroup.  Bound by the counts: those of a bit need the last bit's.
 template <int WAVES, int PER>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void choose_kernel(SelectArgs a) {
   __shared__ int s_count[2][WAVES];
