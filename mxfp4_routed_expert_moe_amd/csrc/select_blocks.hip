@@ -443,7 +443,9 @@ __global__ __launch_bounds__(256) void tile_kernel(SelectArgs a) {
 
 // ---------------------------------------------------------------- choice from the workspace
 // WAVES waves hold 64 * PER scores each, wave w those from 64 * PER * w on.  Where a token
-// and head has one wave, four of them stand in a workgroup.  Bound by the counts: those of a bit need the last bit's.
+// and head has one wave, four of them stand in a workgroup.  Bound by the counts'
+// vector work: two bits at a time, three thresholds in half as many counts, took longer (1021 tokens of 1024 pages
+// 42.9 us for the call against 42.0, one of 16384 pages 44.0 against 39.9).
 template <int WAVES, int PER>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void choose_kernel(SelectArgs a) {
   __shared__ int s_count[2][WAVES];
