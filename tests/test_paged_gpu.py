@@ -300,7 +300,10 @@ GROUPS = [
     ([1] * 40, [600 + 7 * i for i in range(40)], [0, 40], [576], 8, 2, 64, 64),
     # own keys that begin inside a tile of 64, and end in its first, second and last 16
     ([1, 1, 1], [230, 195, 300], [0, 3], [106], 2, 1, 64, 16), ([9, 40], [300, 470], [0, 2], [250], 4, 2, 128, 16),
-    ([2, 70], [330, 305], [0, 2], [165], 2, 1, 256, 32), ([0, 3], [190, 230], [0, 2], [106], 2, 1, 256, 16)]
+    ([2, 70], [330, 305], [0, 2], [165], 2, 1, 256, 32), ([0, 3], [190, 230], [0, 2], [106], 2, 1, 256, 16),
+    # many tiles whose own keys fill a piece but for what is left of the prefix's page; chunks of wide heads behind many pieces
+    ([1] * 40, [2024 - 3 * i for i in range(40)], [0, 40], [1000], 8, 8, 64, 64),
+    ([30, 20, 40], [2300, 2250, 2292], [0, 3], [2048], 16, 4, 256, 64)]
 
 
 @pytest.mark.parametrize("lq,lk,cu,prefix,Hq,Hkv,D,page", GROUPS)
