@@ -732,10 +732,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(Paged
     splits = (all + chunk - 1) / chunk;  // that have keys to see
     if (!prefix && a.n_groups > 0 && split == 0 && w.own == 0)
       for (int i = 0; i < a.prefix_splits; ++i) empty(i);
-    if (split >= max(splits, a.n_groups > 0 ? 0 : 1)) {
-      if (a.n_groups > 0) empty(slot);
-      return;
-    }
+    const SplitWork work = split_work(split, splits, a.slots, a.n_groups > 0);
+    if (work == SplitWork::kEmpty) return empty(slot);
+    if (work == SplitWork::kNothing) return;
     kbeg = w.own + split * chunk, kend = kbeg + min(all - split * chunk, chunk);
   }
 

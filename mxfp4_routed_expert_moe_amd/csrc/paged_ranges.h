@@ -57,4 +57,15 @@ __host__ __device__ inline GroupRange group_range(const int32_t* cu_group, int g
   return r;
 }
 
+// What a block does with split `split` of a tile that sees the keys of `splits` splits (0: none), where a row
+// has `slots` shares: attend to it, write an empty share in its place, or nothing.  every_slot: the join reads all
+// of a row's shares, so each of them is written.  A row of one share has no shares in the workspace, which there
+// may be none of: its tile writes the output itself, also where it sees nothing.
+enum class SplitWork { kAttend, kEmpty, kNothing };
+__host__ __device__ inline SplitWork split_work(int split, int splits, int slots, bool every_slot) {
+  const bool shares = every_slot && slots > 1;
+  if (split < splits || (split == 0 && !shares)) return SplitWork::kAttend;
+  return shares ? SplitWork::kEmpty : SplitWork::kNothing;
+}
+
 }  // namespace moe

@@ -326,6 +326,44 @@ def test_shared_prefix(lq, lk, cu, prefix, Hq, Hkv, D, page):
     assert torch.all(out[sum(lq):] == 9) and torch.all(lse[sum(lq):] == 3)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(8, 2, 128, 64), (2, 2, 64, 16), (4, 1, 256, 32), (4, 4, 128, 128)])
+@pytest.mark.parametrize("lq,lk,cu,prefix,max_kv", [
+    ([1], [0], [0, 1], [0], 8), ([1, 1, 1, 1], [0, 5, 0, 1], [0, 2, 4], [0, 0], 9), ([200], [50], [0, 1], [0], 50),
+    ([1, 40, 0, 1], [3, 30, 0, 0], [1, 4], [15], 20), ([130, 2], [1, 0], [0, 1, 2], [0, 0], 1), ([3], [2], [0, 1], [9], 0)])
+def test_groups_that_share_nothing_in_one_piece(lq, lk, cu, prefix, max_kv, Hq, Hkv, D, page):
+    """Groups without a whole page, over so few keys that a row has one share and the call needs no workspace: rows
+    that see no key get their zeros."""
+    _say("groups in one piece", lq, lk, cu, prefix, max_kv, Hq, Hkv, D, page)
+    g = np.random.default_rng(sum(lq) + D)
+    table, n_pages = _table(g, lk, page)
+    kp, vp, kt, vt = _pool(g, n_pages, page, Hkv, D)
+    q = AR.bf16(g.normal(0, 2, (sum(lq) + 2, Hq, D)))
+    seqs = _seqs(lq, lk)
+    of = [0] * len(lk)
+    for i, j, p in zip(cu, cu[1:], prefix):
+        of[i:j] = [p] * (j - i)
+    out = torch.full(q.shape, 9.0, dtype=BF, device="cuda")
+    assert P.paged_attention_workspace_size(_bf16(q), kt, len(lq), max(lq), max_kv, n_groups=len(prefix), max_prefix=max(prefix)) == 0
+    _, lse = _run(_bf16(q), kt, vt, table, seqs, cu_group=_i32(cu), prefix_len=_i32(prefix), max_prefix=max(prefix), max_kv=max_kv,
+                  out=out)
+    see = PR.visible(seqs, table, page, n_pages, Hkv, prefix=of, max_prefix=max(prefix), max_kv=max_kv)
+    _check(out, lse, q, kp, vp, table, seqs, see, D ** -0.5)
+    assert torch.all(out[sum(lq):] == 9) and torch.all(lse[sum(lq):] == 3)
+
+
+@pytest.mark.parametrize("pages,width,max_kv", [(0, 2, 100), (5, 0, 0)])
+def test_groups_over_an_empty_cache(pages, width, max_kv):
+    """A pool without pages, and a table without entries: every row sees nothing."""
+    _say("groups, empty cache", pages, width)
+    pool = torch.zeros(pages, 64, 2, 128, dtype=BF, device="cuda")
+    q = torch.ones(3, 8, 128, dtype=BF, device="cuda")
+    lse = torch.full((3, 8), 3.0, device="cuda")
+    args = q, pool, pool, _i32([0, 1, 3]), _i32([50, 2]), torch.zeros(2, width, dtype=torch.int32, device="cuda"), 2, max_kv
+    assert P.paged_attention_workspace_size(q, pool, 2, 2, max_kv, n_groups=1) == 0
+    out = P.paged_attention(*args, cu_group=_i32([0, 2]), prefix_len=_i32([0]), lse=lse)
+    assert torch.all(out == 0) and torch.all(lse == -float("inf"))
+
+
 def _blocks(g, seqs, T, Hkv, page, n, junk=True):
     """Lists of blocks: distinct ones, and now and then one twice, out of order, past the row's end, below 0, or none at all."""
     out = np.full((T, Hkv, n), -1)

@@ -82,3 +82,37 @@ def test_groups_stay_inside(lib):
         first = np.clip(cu[:-1].astype(np.int64), 0, n_seqs)
         assert np.array_equal(out[:, 0], first)
         assert np.array_equal(out[:, 1], np.maximum(np.clip(cu[1:].astype(np.int64), 0, n_seqs), first))
+
+
+WORK = """
+#define __host__
+#define __device__
+#include "paged_ranges.h"
+extern "C" int work(int split, int splits, int slots, int every_slot) {
+  return static_cast<int>(moe::split_work(split, splits, slots, every_slot));
+}
+"""
+ATTEND, EMPTY, NOTHING = range(3)
+
+
+def test_shares_of_a_row(tmp_path):
+    """A row of one share never has one in the workspace, and its output is written by exactly one block; of several, where
+    the join reads them all, every one is written."""
+    gxx = shutil.which("g++")
+    if not gxx:
+        pytest.skip("needs g++")
+    src, so = str(tmp_path / "work.cpp"), str(tmp_path / "work.so")
+    with open(src, "w") as f:
+        f.write(WORK)
+    subprocess.run([gxx, "-O1", "-std=c++17", "-shared", "-fPIC", "-I", CSRC, src, "-o", so], check=True)
+    work = ctypes.CDLL(so).work
+    for slots in range(1, 6):
+        for launched in range(1, slots + 1):  # splits of the launch; the other slots are a prefix's
+            for splits in range(launched + 1):  # that the tile has keys for
+                done = [work(s, splits, slots, 1) for s in range(launched)]
+                if slots == 1:
+                    assert done == [ATTEND]
+                else:
+                    assert done == [ATTEND] * splits + [EMPTY] * (launched - splits)
+                some = max(splits, 1)  # without groups the join reads the splits that there are
+                assert [work(s, splits, slots, 0) for s in range(launched)] == [ATTEND] * some + [NOTHING] * (launched - some)
