@@ -155,7 +155,10 @@ typedef struct moe_paged_attn {
 } moe_paged_attn;
 
 /* Depends on the shape fields only (heads, head_dim, n_seqs, q_rows, page_size, max_*,
- * n_groups, n_blocks); 0 for a shape that needs none or is not supported. */
+ * n_groups, n_blocks); 0 for a shape that needs none or is not supported.  Not supported (MOE_ESHAPE), besides
+ * what the fields say: q_rows * q_heads of 2^30 or more, and launches of 2^24 blocks of threads or more (one per
+ * row tile, key head and piece of the keys; where keys come in pieces, one per 1024 / head_dim rows for their
+ * join, one per row where the pieces are more than 16). */
 size_t moe_paged_attention_workspace_size(const moe_paged_attn* a);
 
 /* ws: at least that many bytes, 256-byte aligned (may be NULL when that is 0). */

@@ -1107,6 +1107,14 @@ size_t part_bytes(const moe_paged_attn& d, const Plan& p) {
   return align256(rows * d.p.head_dim * 4) + align256(rows * 8);
 }
 
+// Rows of a block of the join, and its blocks.
+int join_rows(const moe_paged_attn& d, const Plan& p) { return p.slots() > kJoinShared ? 1 : 256 / (d.p.head_dim / 4); }
+int64_t join_blocks(const moe_paged_attn& d, const Plan& p) {
+  if (p.slots() <= 1) return 0;
+  const int64_t rows = (p.token ? static_cast<int64_t>(d.p.n_seqs) * d.max_q : d.p.q_rows) * d.p.q_heads;
+  return ceil_div(rows, join_rows(d, p));
+}
+
 // The shape fields, which the workspace depends on.
 int check_shape(const moe_paged_attn* a) {
   if (!a) return MOE_EINVAL;
@@ -1120,7 +1128,7 @@ int check_shape(const moe_paged_attn* a) {
   if (a->n_blocks > 0 && a->max_kv > static_cast<int64_t>(32 * kWords) * a->p.page_size) return MOE_ESHAPE;
   const Plan p = make_plan(*a);
   // grid limits: 2^32 threads along x, 65535 blocks along y
-  if (p.units() > 0xffffff / a->p.kv_heads || p.splits > 65535) return MOE_ESHAPE;
+  if (p.units() > 0xffffff / a->p.kv_heads || p.splits > 65535 || join_blocks(*a, p) > 0xffffff) return MOE_ESHAPE;
   if (static_cast<int64_t>(a->p.q_rows) * a->p.q_heads > 0x3fffffff) return MOE_ESHAPE;
   return MOE_OK;
 }
@@ -1144,7 +1152,7 @@ void launch_rows(const PagedArgs& a, unsigned blocks, hipStream_t s) {
 }
 
 template <int D>
-void launch(const PagedArgs& a, const Plan& p, hipStream_t s) {
+void launch(const PagedArgs& a, const Plan& p, int64_t joins, hipStream_t s) {
   if (p.token) {
     const dim3 grid(static_cast<unsigned>(p.tiles * a.kv_heads), static_cast<unsigned>(p.splits));
     const bool whole = 1 << a.s.shift >= kKeysT;
@@ -1160,10 +1168,7 @@ void launch(const PagedArgs& a, const Plan& p, hipStream_t s) {
       default: launch_rows<D, 1>(a, blocks, s); break;
     }
   }
-  if (a.slots > 1) {
-    const int64_t rows = (a.token ? static_cast<int64_t>(a.s.n_seqs) * a.max_q : a.s.q_rows) * a.q_heads;
-    paged_join_kernel<D><<<static_cast<unsigned>(ceil_div(rows, a.join_rows)), 256, 0, s>>>(a);
-  }
+  if (joins > 0) paged_join_kernel<D><<<static_cast<unsigned>(joins), 256, 0, s>>>(a);
 }
 
 }  // namespace
@@ -1214,14 +1219,15 @@ int moe_paged_attention(const moe_paged_attn* a, void* ws, size_t ws_bytes, void
   k.units = static_cast<int>(plan.units()), k.prefix_units = static_cast<int>(plan.prefix_units());
   k.token = plan.token;
   k.tile_rows = plan.token ? moe::kRowsT : moe::kRowsP;
-  k.join_rows = plan.slots() > moe::kJoinShared ? 1 : 256 / (p.head_dim / 4);
+  k.join_rows = moe::join_rows(*a, plan);
   k.scale = a->scale;
   k.c = a->scale * 1.44269504088896340736f;  // log2(e)
+  const int64_t joins = moe::join_blocks(*a, plan);
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   switch (p.head_dim) {
-    case 64: moe::launch<64>(k, plan, s); break;
-    case 128: moe::launch<128>(k, plan, s); break;
-    default: moe::launch<256>(k, plan, s); break;
+    case 64: moe::launch<64>(k, plan, joins, s); break;
+    case 128: moe::launch<128>(k, plan, joins, s); break;
+    default: moe::launch<256>(k, plan, joins, s); break;
   }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
 }

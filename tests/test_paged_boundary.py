@@ -219,3 +219,17 @@ def test_reference_selection():
     pick = lambda n, first, last: PR.select(q, bounds, table, [(0, 1, 9 * 16)], 16, n, first, last)[0, 0].tolist()  # noqa: E731
     assert pick(3, 1, 1) == [0, 4, 8] and pick(4, 0, 1) == [1, 2, 4, 8] and pick(3, 0, 1) == [1, 4, 8]
     assert pick(8, 0, 1) == [0, 1, 2, 3, 4, 5, 6, 8] and pick(10, 0, 1) == [0, 1, 2, 3, 4, 5, 6, 7, 8, -1]
+
+
+def test_attention_join_fits_a_launch():
+    """Rows in shares whose join would need 2^32 threads are refused before anything runs, and need no workspace; as many
+    rows of one share are not."""
+    rows = dict(q_rows=B.MOE_MAX_TOKENS, head_dim=64, q_heads=1024, kv_heads=1024)
+    many = dict(rows, n_groups=1, cu_group=FAKE, prefix_len=FAKE, max_prefix=1280)
+    spread = dict(n_seqs=65536, q_rows=65536, max_q=32, head_dim=128, q_heads=64, kv_heads=64, table_pages=1024, table_stride=1024,
+                  max_kv=65536, n_blocks=32, blocks=FAKE)
+    for bad in (spread, many):
+        assert _attn(**bad) == ESHAPE
+        assert P.lib().moe_paged_attention_workspace_size(ctypes.byref(_attn_desc(**bad))) == 0
+    fits = dict(many, q_heads=512, kv_heads=512)
+    assert P.lib().moe_paged_attention_workspace_size(ctypes.byref(_attn_desc(**fits))) == 2 * B.MOE_MAX_TOKENS * 512 * (64 * 4 + 8)
