@@ -210,6 +210,9 @@ class AttentionBlock:
         """Room in the cache for sequences that grow to `ends`, and by up to `more` tokens in steps of
         an advanced plan: every sequence has its max_len rows."""
 
+    def _check_rows(self, plan: Plan):
+        """Whether the plan's sequences may write its rows: every sequence has rows of its own."""
+
     def workspace(self, plan: Plan):
         """The attention workspace of a plan, for callers that keep it."""
         n = plan.rows.numel()
@@ -227,6 +230,7 @@ class AttentionBlock:
         if plan.longest > plan.max_kv:
             raise ValueError(f"the plan was advanced to {plan.longest} tokens, its bound is {plan.max_kv}")
         plan._check()
+        self._check_rows(plan)
         y = self._enqueue(x, plan, ws)
         plan._ran()
         for b in plan._sequences():
@@ -254,7 +258,8 @@ class PagedAttentionBlock(AttentionBlock):
     A plan gives its sequences the pages that they will fill (those of an advanced plan for
     all of its steps), `reset` gives them back, `fork` lets a sequence begin as another one, in the
     same pages.  Neighbouring sequences that share pages are attended to as a group: what they
-    share is read once for all of them.
+    share is read once for all of them.  No sequence writes to a page that another one holds: a plan that would
+    (one that ran before the fork, run again) is refused, a replay of its graph stores nothing there.
 
     select (n_blocks, first, last): single-token plans attend to n_blocks pages of each sequence,
     its first and last ones and those whose keys' bounds promise the most; None: to everything."""
@@ -276,7 +281,9 @@ class PagedAttentionBlock(AttentionBlock):
         self.cache = torch.zeros((self.n_pages, self.page_size, 2 * Hkv, D), dtype=bf16, device=dev)
         self.k_pages, self.v_pages = self.cache[:, :, :Hkv], self.cache[:, :, Hkv:]
         self.bounds = None if self.select is None else torch.zeros((self.n_pages, 2, Hkv, D), dtype=bf16, device=dev)
-        self.table = torch.full((self.max_seqs, -(-self.max_len // self.page_size)), -1, dtype=torch.int32, device=dev)
+        # the pages of a sequence, and those of them that it may write to: no other one holds them
+        self.tables = torch.full((2, self.max_seqs, -(-self.max_len // self.page_size)), -1, dtype=torch.int32, device=dev)
+        self.table, self.own = self.tables
         self.pages = [[] for _ in range(self.max_seqs)]  # of every sequence, in order
         self.free = list(range(self.n_pages - 1, -1, -1))
         self.users = [0] * self.n_pages  # sequences that hold a page
@@ -296,25 +303,36 @@ class PagedAttentionBlock(AttentionBlock):
 
     def _take(self, b, pages):
         """These pages are the next ones of sequence b."""
-        have = len(self.pages[b])
         for page in pages:
             self.users[page] += 1
         self.pages[b] += pages
-        self.table[b, have:have + len(pages)] = torch.tensor(pages, dtype=torch.int32, device=self.table.device)
+        self._name(b, len(self.pages[b]) - len(pages))
+
+    def _name(self, b, begin=0):
+        """The pages of sequence b from its page `begin` on, to the tables."""
+        pages = self.pages[b][begin:]
+        own = [p if self.users[p] == 1 else -1 for p in pages]
+        self.tables[:, b, begin:begin + len(pages)] = torch.tensor([pages, own], dtype=torch.int32, device=self.table.device)
 
     def reset(self, b=None):
         super().reset(b)
+        left = set()  # pages with one holder less
         for s in range(self.max_seqs) if b is None else (b,):
             for page in self.pages[s]:
                 self.users[page] -= 1
                 if not self.users[page]:
                     self.free.append(page)
+            left.update(self.pages[s])
             self.pages[s] = []
-            self.table[s].fill_(-1)
+            self.tables[:, s].fill_(-1)
+        for s, pages in enumerate(self.pages):
+            if not left.isdisjoint(pages):
+                self._name(s)
 
     def fork(self, src: int, dst: int):
         """Sequence dst, which holds nothing, begins as a copy of what src holds: in the same pages, but for
-        the last one where it is not full (a copy on the current stream).  The plans of src have run."""
+        the last one where it is not full (a copy on the current stream).  The plans of src have run; those whose rows are
+        in the shared pages do not run again while both hold them."""
         for b in (src, dst):
             if not 0 <= b < self.max_seqs:
                 raise ValueError(f"there are {self.max_seqs} sequences, got {b}")
@@ -328,6 +346,7 @@ class PagedAttentionBlock(AttentionBlock):
             raise ValueError("no page is free for a copy of the last one")
         if full:
             self._take(dst, self.pages[src][:full])
+            self._name(src)
         if rest:
             page, old = self.free.pop(), self.pages[src][full]
             self._take(dst, [page])
@@ -338,6 +357,7 @@ class PagedAttentionBlock(AttentionBlock):
 
     def plan(self, new, max_kv=None) -> Plan:
         plan = super().plan(new, max_kv)
+        plan.begins = {b: self.lens[b] - plan.new[b] for b in plan._sequences()}
         cu, prefix = self._groups(plan._sequences(), len(plan.new))
         more = 0 if plan.max_q > 1 else plan.max_kv - plan.longest
         of = {}
@@ -370,6 +390,12 @@ class PagedAttentionBlock(AttentionBlock):
                 shared.append(None)  # alone
         return cu + [end], [(n or 0) * self.page_size for n in shared]
 
+    def _check_rows(self, plan: Plan):
+        for b, begin in plan.begins.items():
+            first, last = (p // self.page_size for p in (begin + plan.steps, begin + plan.steps + plan.new[b] - 1))
+            if any(self.users[p] > 1 for p in self.pages[b][first:last + 1]):
+                raise ValueError(f"the plan would write to pages of sequence {b} that another one holds: make a new plan")
+
     def workspace(self, plan: Plan):
         """The workspaces of a plan's selection and attention, for callers that keep them."""
         n = plan.rows.numel()
@@ -390,9 +416,9 @@ class PagedAttentionBlock(AttentionBlock):
         q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
         select_ws, attention_ws = ws or (None, None)
         n = plan.cu_q.numel() - 1
-        at = plan.cu_q, plan.kv_len, self.table[:n]
+        at, own = (plan.cu_q, plan.kv_len, self.table[:n]), (plan.cu_q, plan.kv_len, self.own[:n])
         A.fp8_linear(x, self.w_qkv, self.qkv_scale, y=qkv.view(T, -1), ws=self.ws)
-        P.paged_append(k, v, self.k_pages, self.v_pages, *at, q=q, q_out=q, bounds=self.bounds, q_weight=self.q_weight,
+        P.paged_append(k, v, self.k_pages, self.v_pages, *own, q=q, q_out=q, bounds=self.bounds, q_weight=self.q_weight,
                        k_weight=self.k_weight, cos_sin=self.cos_sin, **self.rope)
         if self._selects(plan):
             blocks = self.blocks[:T]

@@ -136,3 +136,36 @@ def test_replays_past_the_pages_store_nothing():
     torch.cuda.synchronize()
     others = [p for p in range(9) if p not in own]
     assert torch.equal(b.cache[others], before[others])
+
+
+def test_replays_of_a_forked_prompt_leave_its_pages_alone():
+    """A captured prompt that is replayed after a fork stores nothing to the pages that both sequences hold; its own last page, and
+    after the other sequence has gone all of them, it writes."""
+    _say("replays after a fork")
+    b, _ = _blocks(4, 2, 64, page_size=16, max_seqs=2, n_pages=20, max_len=200)
+    x, prompt = _x(60, 272, 1), b.plan([60])
+    ws = b.workspace(prompt)
+    b.forward(x, prompt, ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.forward(x, prompt, ws)
+    b.fork(0, 1)
+    with pytest.raises(ValueError):
+        b.forward(x, prompt, ws)
+    shared, last = b.pages[0][:3], b.pages[0][3]
+    before = b.cache.clone()
+    x.copy_(_x(60, 272, 2))
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        others = [p for p in range(20) if p != last]
+        assert torch.equal(b.cache[others], before[others])
+    assert not torch.equal(b.cache[last], before[last])
+    step = b.plan([0, 1])
+    b.forward(_x(1, 272, 3), step)
+    _verify(b, [0, 1], step)
+    b.reset(1)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert not torch.equal(b.cache[shared], before[shared])
+    _verify(b, [60], prompt)

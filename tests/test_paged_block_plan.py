@@ -224,3 +224,72 @@ def test_empty_plan(monkeypatch):
     plan = m.b.plan([])
     assert m.b.forward(torch.zeros(0, HIDDEN).bfloat16(), plan).shape == (0, HIDDEN)
     m.check_pages()
+
+
+def test_a_plan_does_not_run_again_over_shared_pages(monkeypatch):
+    """What a fork shares is written no more: a plan of the sequence that ran before is refused as long as another one holds a
+    page of its rows, and what its replay would store stays out of them."""
+    m = Model(monkeypatch)
+    first = m.step([40])
+    more = m.step([3])
+    again = m.x([40])
+    m.fed[0] = m.fed[0][-40:] + m.fed[0][40:43]  # the first plan runs anew: no fork yet
+    m.b.forward(again, first)
+    assert m.read(m.b.table[0], 43) == [float(t) for t in m.fed[0]]
+    m.fork(0, 1)
+    kept = m.read(m.b.table[1], 43)
+    with pytest.raises(ValueError):
+        m.b.forward(m.x([40]), first)
+    m.b._enqueue(torch.full((40, HIDDEN), 7.0).bfloat16(), first, None)  # as a replay of a graph, which no check sees
+    assert m.read(m.b.table[1], 43) == kept and m.read(m.b.table[0], 32) == kept[:32]
+    m.fed[0] = m.fed[1] + []
+    m.b._enqueue(torch.tensor(m.fed[0][:40]).float()[:, None].expand(40, HIDDEN).bfloat16(), first, None)
+    m.b.forward(torch.tensor(m.fed[0][40:]).float()[:, None].expand(3, HIDDEN).bfloat16(), more)  # in a page of its own
+    m.step([2, 1])
+    m.fork(1, 2)
+    m.b.reset(1)
+    m.fed[1] = []
+    m.check_pages()
+    with pytest.raises(ValueError):
+        m.b.forward(m.x([40]), first)  # sequence 2 still holds the pages
+    m.fed[0] = m.fed[0][:45]
+    m.b.reset(2)
+    m.fed[2] = []
+    tokens = m.fed[0][:40]
+    m.b.forward(torch.tensor(tokens[::-1]).float()[:, None].expand(40, HIDDEN).bfloat16(), first)  # alone again
+    assert m.read(m.b.table[0], 40) == [float(t) for t in tokens[::-1]]
+
+
+def test_a_step_does_not_run_again_into_a_page_that_it_filled(monkeypatch):
+    m = Model(monkeypatch)
+    m.step([31, 5])
+    step = m.b.plan([1, 1], max_kv=40)
+    m.step([1, 1], step)
+    m.fork(0, 2)
+    with pytest.raises(ValueError):
+        m.b.forward(m.x([1, 1]), step)  # token 31 of sequence 0 is in a page that sequence 2 holds
+    m.fed = [f[:n] for f, n in zip(m.fed, (32, 6, 32, 0))]
+    step.advance()
+    m.step([1, 1], step)  # the next one is in a page of its own
+    m.step([0, 0, 4])
+    m.check_pages()
+
+
+def test_the_tables_name_pages_and_what_may_be_written(monkeypatch):
+    """After forks and resets in any order the device tables are what the host knows."""
+    m = Model(monkeypatch, n_pages=30)
+
+    def check():
+        m.check_pages()
+        for s, pages in enumerate(m.b.pages):
+            own = [p if m.b.users[p] == 1 else -1 for p in pages]
+            assert m.b.own[s].tolist() == own + [-1] * (m.b.own.shape[1] - len(own))
+
+    m.step([50])
+    for do in ((m.fork, 0, 2), (m.fork, 2, 1), (m.step, [1, 20, 1]), (m.b.reset, 2), (m.fork, 1, 3), (m.b.reset, 0), (m.b.reset, 3),
+               (m.fork, 1, 0), (m.b.reset,)):
+        do[0](*do[1:])
+        if do[0] == m.b.reset:
+            for s in range(4) if len(do) == 1 else do[1:]:
+                m.fed[s] = []
+        check()
