@@ -90,6 +90,7 @@ class Plan:
             self.block.lens[b] -= self.new[b]
             self.block._unrun[b].pop()
             self.block._owner[b] = 0
+            self.block._give_back(b)
 
     def _sequences(self):
         """The sequences that the plan brings tokens to."""
@@ -210,6 +211,9 @@ class AttentionBlock:
         """Room in the cache for sequences that grow to `ends`, and by up to `more` tokens in steps of
         an advanced plan: every sequence has its max_len rows."""
 
+    def _give_back(self, b):
+        """What the cache kept for a cancelled plan of sequence b: its rows are the sequence's all the same."""
+
     def _check_rows(self, plan: Plan):
         """Whether the plan's sequences may write its rows: every sequence has rows of its own."""
 
@@ -256,10 +260,11 @@ class PagedAttentionBlock(AttentionBlock):
     """AttentionBlock over a cache of n_pages pages of page_size tokens.
 
     A plan gives its sequences the pages that they will fill (those of an advanced plan for
-    all of its steps), `reset` gives them back, `fork` lets a sequence begin as another one, in the
-    same pages.  Neighbouring sequences that share pages are attended to as a group: what they
-    share is read once for all of them.  No sequence writes to a page that another one holds: a plan that would
-    (one that ran before the fork, run again) is refused, a replay of its graph stores nothing there.
+    all of its steps); `Plan.cancel` gives those back that the sequence's tokens do not need, `reset` all of
+    them.  `fork` lets a sequence begin as another one, in the same pages.  Neighbouring sequences that share
+    pages are attended to as a group: what they share is read once for all of them.  No sequence writes to a page
+    that another one holds: a plan that would (one that ran before the fork, run again) is refused, a
+    replay of its graph stores nothing there.
 
     select (n_blocks, first, last): single-token plans attend to n_blocks pages of each sequence,
     its first and last ones and those whose keys' bounds promise the most; None: to everything."""
@@ -313,6 +318,14 @@ class PagedAttentionBlock(AttentionBlock):
         pages = self.pages[b][begin:]
         own = [p if self.users[p] == 1 else -1 for p in pages]
         self.tables[:, b, begin:begin + len(pages)] = torch.tensor([pages, own], dtype=torch.int32, device=self.table.device)
+
+    def _give_back(self, b):
+        keep = -(-self.lens[b] // self.page_size)
+        for page in self.pages[b][keep:]:  # never shared: forks share pages of tokens that there are
+            self.users[page] -= 1
+            self.free.append(page)
+        del self.pages[b][keep:]
+        self.tables[:, b, keep:].fill_(-1)
 
     def reset(self, b=None):
         super().reset(b)

@@ -293,3 +293,54 @@ def test_the_tables_name_pages_and_what_may_be_written(monkeypatch):
             for s in range(4) if len(do) == 1 else do[1:]:
                 m.fed[s] = []
         check()
+
+
+def test_cancelled_plans_give_their_pages_back(monkeypatch):
+    """Those that no token of the sequence's other plans needs: also the ones kept for steps of an advanced plan, and not
+    those of a plan that has yet to run, or shared ones."""
+    m = Model(monkeypatch, n_pages=10)
+    plan = m.b.plan([150])
+    assert not m.b.free
+    plan.cancel()
+    m.check_pages()
+    assert m.b.pages[0] == []
+    m.step([20, 20])  # the pages are there again
+    steps = m.b.plan([1, 1], max_kv=60)
+    assert [len(p) for p in m.b.pages] == [4, 4, 0, 0]
+    steps.cancel()
+    m.check_pages()
+    assert [len(p) for p in m.b.pages] == [2, 2, 0, 0]
+    first, second = m.b.plan([20]), m.b.plan([50])
+    assert len(m.b.pages[0]) == 6
+    second.cancel()
+    m.check_pages()
+    assert len(m.b.pages[0]) == 3  # 40 tokens, 20 of them in the plan that runs now
+    m.step([20], first)
+    m.fork(0, 2)
+    plan = m.b.plan([0, 10, 40])
+    m.b.reset(1)
+    m.fed[1] = []
+    plan.cancel()
+    m.check_pages()
+    assert [len(p) for p in m.b.pages] == [3, 0, 3, 0] and m.b.pages[2][:2] == m.b.pages[0][:2]
+    m.step([1, 0, 1])
+    m.fork(1, 3)
+
+
+def test_a_cancelled_step_gives_back_what_was_kept_for_it(monkeypatch):
+    """An advanced plan ends with a plan behind it, so a cancel of that one leaves the sequence what its tokens need."""
+    m = Model(monkeypatch, n_pages=8)
+    m.step([15])
+    step = m.b.plan([1], max_kv=100)
+    for i in range(3):
+        m.step([1], step)
+        if i < 2:
+            step.advance()
+    assert len(m.b.pages[0]) == 7
+    m.b.plan([2]).cancel()
+    m.check_pages()
+    assert len(m.b.pages[0]) == 2
+    with pytest.raises(ValueError):
+        step.advance()
+    m.step([100])
+    m.check_pages()
