@@ -296,7 +296,13 @@ class PagedAttentionBlock(AttentionBlock):
             self.blocks = torch.empty((self.max_tokens, Hkv, self.select[0]), dtype=torch.int32, device=dev)
 
     def _reserve(self, new, ends, more):
-        more = 0 if any(n > 1 for n in new) else more  # only single-token plans are advanced
+        single = not any(n > 1 for n in new)
+        if self.select is not None and single:
+            longest = max((e for e, n in zip(ends, new) if n), default=0) + more
+            if longest > 32768 * self.page_size or sum(new) * self.Hkv >= 1 << 23:  # select_blocks' limits
+                raise ValueError(f"select ranks up to 32768 pages a sequence, for fewer than 2^23 tokens x key heads: the plan has "
+                                 f"{-(-longest // self.page_size)} pages, {sum(new)} x {self.Hkv}")
+        more = more if single else 0  # only single-token plans are advanced
         grow = [(b, -(-min(e + more, self.max_len) // self.page_size) - len(self.pages[b]))
                 for b, (n, e) in enumerate(zip(new, ends)) if n]
         need = sum(max(n, 0) for _, n in grow)

@@ -344,3 +344,18 @@ def test_a_cancelled_step_gives_back_what_was_kept_for_it(monkeypatch):
         step.advance()
     m.step([100])
     m.check_pages()
+
+
+def test_selection_past_its_limits_is_refused_with_the_plan(monkeypatch):
+    """More blocks than the choice can rank: the plan is refused before it takes pages, not its run after the append."""
+    m = Model(monkeypatch, max_len=32768 * 16 + 100, n_pages=64, select=(4, 1, 2))
+    m.step([100, 30])
+    for bound in (32768 * 16 + 1, 32768 * 16 + 100):
+        with pytest.raises(ValueError, match="32768"):
+            m.b.plan([1, 1], max_kv=bound)
+        with pytest.raises(ValueError, match="free"):
+            m.b.plan([1, 1], max_kv=bound - 101)  # not past the limit: refused for want of pages
+    m.check_pages()
+    m.step([1, 1], m.b.plan([1, 1], max_kv=200))
+    m.step([2, 1], m.b.plan([2, 1], max_kv=32768 * 16 + 100))  # selects nothing
+    m.check_pages()
