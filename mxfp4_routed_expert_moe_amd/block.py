@@ -267,7 +267,8 @@ class PagedAttentionBlock(AttentionBlock):
     replay of its graph stores nothing there.
 
     select (n_blocks, first, last): single-token plans attend to n_blocks pages of each sequence,
-    its first and last ones and those whose keys' bounds promise the most; None: to everything."""
+    its first and last ones and those whose keys' bounds promise the most, read for each sequence on its own, also
+    where sequences share them; None: to everything."""
 
     def __init__(self, *args, page_size: int = 64, n_pages: int, select=None, **kw):
         self.page_size, self.n_pages, self.select = page_size, n_pages, select
@@ -377,6 +378,9 @@ class PagedAttentionBlock(AttentionBlock):
     def plan(self, new, max_kv=None) -> Plan:
         plan = super().plan(new, max_kv)
         plan.begins = {b: self.lens[b] - plan.new[b] for b in plan._sequences()}
+        plan.group, plan.max_prefix, plan.max_own = None, 0, plan.max_kv
+        if self._selects(plan):  # every sequence's chosen pages are read for itself
+            return plan
         cu, prefix = self._groups(plan._sequences(), len(plan.new))
         more = 0 if plan.max_q > 1 else plan.max_kv - plan.longest
         of = {}
@@ -384,7 +388,6 @@ class PagedAttentionBlock(AttentionBlock):
             of.update(dict.fromkeys(range(i, j), p))
         plan.max_prefix = max(prefix, default=0)
         plan.max_own = max((min(self.lens[b] + more, self.max_len) - of[b] for b in plan._sequences()), default=0)
-        plan.group = None
         if plan.max_prefix:
             i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=self.cache.device)  # noqa: E731
             plan.group = i32(cu), i32(prefix)

@@ -359,3 +359,17 @@ def test_selection_past_its_limits_is_refused_with_the_plan(monkeypatch):
     m.step([1, 1], m.b.plan([1, 1], max_kv=200))
     m.step([2, 1], m.b.plan([2, 1], max_kv=32768 * 16 + 100))  # selects nothing
     m.check_pages()
+
+
+def test_selecting_plans_have_no_groups(monkeypatch):
+    """Every sequence's chosen pages are read for itself: nothing is made for groups that no call reads."""
+    m = Model(monkeypatch, select=(4, 1, 2))
+    m.step([100])
+    m.fork(0, 1)
+    assert m.b.plan([1, 1]).group is None
+    m.b.reset()
+    m.fed = [[] for _ in m.fed]
+    m.step([100])
+    m.fork(0, 1)
+    m.step([2, 1])
+    assert m.calls[-1][5] == ([0, 2], [96], 96)
