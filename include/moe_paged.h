@@ -122,7 +122,8 @@ int moe_paged_append(const moe_append* a, void* stream);
  * Shared prefixes.  cu_group int32 [n_groups + 1] (device) cuts the sequences into
  * groups of consecutive ones; the first prefix_len[g] keys of all sequences of
  * group g are the same, and in the same pages where they fill pages, so these are
- * read through the table row of the group's first sequence, once for all rows.  (A
+ * read through the table row of the group's first sequence, once for all rows: that row names
+ * all of them, also where the sequence itself is shorter.  (A
  * sequence shorter than prefix_len holds the first of these pages, the last in part.)
  * n_groups = 0 (cu_group and prefix_len may then be NULL), or sequences outside
  * every group: no shared prefix.  The result does not depend on the grouping but

@@ -351,8 +351,9 @@ class PagedAttentionBlock(AttentionBlock):
 
     def fork(self, src: int, dst: int):
         """Sequence dst, which holds nothing, begins as a copy of what src holds: in the same pages, but for
-        the last one where it is not full (a copy on the current stream).  The plans of src have run; those whose rows are
-        in the shared pages do not run again while both hold them."""
+        the last one where it is not full (a copy on the current stream).  The plans of src have run, and the replays that
+        were noted for them are enqueued; those whose rows are in the shared pages do not run again while both
+        hold them."""
         for b in (src, dst):
             if not 0 <= b < self.max_seqs:
                 raise ValueError(f"there are {self.max_seqs} sequences, got {b}")

@@ -16,9 +16,10 @@
 // with a sum of 0, so the join needs to know nothing about groups or lists.
 //
 // A sequence alone costs what it does over a contiguous cache (us, pages of 64; contiguous): 64 tokens over up to
-// 8192 keys 216, 212; 4 over 1024 10.8, 10.6; one over 65536 57, 57; a prompt of 4096 152, 151; with pages of 16,
-// a lookup per 16 keys, 219 and 147.  Heads of 256 lose more, 25 and 22 for one token over 32768 keys, 202 and 177 for
-// a prompt of 4096: all registers are in use, and the addresses are made anew for every tile.
+// 8192 keys 216, 212; 4 over 1024 10.9, 10.5; one over 65536 57 to 60, 57 to 61; a prompt of 4096 147 to 152, 146 to
+// 151; with pages of 16, a lookup per 16 keys, 219 and 142 to 147.  Heads of 256 lose more, 25 and 22 for one token over
+// 32768 keys, 202 and 177 for a prompt of 4096: the addresses are made anew for every tile, and some 50 registers
+// still spill (the contiguous kernel's do not).
 #include <math.h>
 
 #include <algorithm>
@@ -638,14 +639,15 @@ constexpr int kRowsP = 128;  // rows of a block: 4 waves x 32
 constexpr int kKeysP = 64;   // keys of a tile
 
 // 4 waves x 32 rows and tiles of 64 keys that all of them read: 2 x 32 KB of LDS at heads of 128, two blocks on a
-// CU, one's softmax under the other's products.  A prefix of 16384 keys under 1100 rows of 32 heads: 296 us for the
-// whole call, 0.92 PFLOP/s (matrix pipes busy 45 %, vector pipes 41 %).  Listed blocks are masked
-// tiles throughout, as neighbouring tokens list most pages together but not all (509 tokens, 40 pages of 32 each: 48 us; in
+// CU, one's softmax under the other's products.  A prefix of 16384 keys under 1003 rows of 32 heads: 293 to 304 us for the
+// whole call, 0.94 to 0.90 PFLOP/s (matrix pipes busy 45 %, vector pipes 41 %).  Listed blocks are masked
+// tiles throughout, also the third of them that every token of a wave lists whole (509 tokens, 40 pages of 32 each: 48 us; in
 // 32-row tiles 94).
 // A launch has units of kv_heads blocks each: (tile, split) pairs of sequences over their
 // own keys, or over listed blocks, and behind them those of groups over their prefixes.
-// (64 single tokens behind a prefix of 16384, whole call: 101 us; prefix first 113; the kinds evenly mixed 113 to
-// 126, as a block that multiplies then waits for its keys behind those that stream the caches.)
+// (64 single tokens behind a prefix of 16384, whole call, before its pieces had their present sizes, 99 now: 101 us;
+// prefix first 113; the kinds evenly mixed 113 to 126, as a block that multiplies then waits for its keys behind
+// those that stream the caches.)
 template <int D, bool LISTED, int N>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void paged_rows_kernel(PagedArgs a) {
   constexpr int kTile = kKeysP * 2 * D;
@@ -1086,8 +1088,9 @@ Plan make_plan(const moe_paged_attn& d) {
     p.prefix_tiles = tile_bound(s.q_rows * g, std::min<int64_t>(d.n_groups, s.q_rows));
     const int64_t blocks = p.prefix_tiles * s.kv_heads;
     // One block a CU, or two where that gains more than the shares of twice the splits cost: a second block on a CU
-    // hides about a third of a tile's 400 ns (heads of 256, which have a CU each: its smaller pieces leave less at the end).  256
+    // hides about a third of a tile's 400 ns.  256
     // blocks, 512: eight chunks of up to 256 behind 16384 432, 295; four of 64 behind 8192 44, 48; heads of 256, three of 200 164, 150.
+    // Those have one block on a CU either way, so what they gain is smaller pieces at the end; the 800 is fitted to that case alone.
     const int64_t splits = std::max<int64_t>(kCus / std::max<int64_t>(blocks, 1), 1);
     const int64_t gain = blocks * ceil_div(d.max_prefix, kKeysP) / kCus * (s.head_dim == 256 ? 800 : s.head_dim);
     const int64_t cost = splits * 8 * s.q_rows * s.q_heads * s.head_dim / 5000;  // ns: stored and loaded once at 5 TB/s

@@ -226,7 +226,8 @@ def paged_attention(q, k_pages, v_pages, cu_q, kv_len, page_table, max_q: int, m
 
     max_q: the bound on a sequence's new rows; max_kv: on its keys, behind its shared prefix where there is one.
     cu_group int32 [groups + 1] with prefix_len int32 [groups] and their bound max_prefix: the sequences of a
-    group, consecutive ones, hold the same first prefix_len keys in the same pages.
+    group, consecutive ones, hold the same first prefix_len keys in the same pages, all of them named by the
+    first one's row of the table.
     blocks int32 [T, Hkv, n]: the blocks that each token and key head sees (select_blocks).
     scale: default D ** -0.5.  lse: float32 [T, Hq] to fill, or None.  Rows of out that belong
     to no sequence are left as they are (new: undefined)."""
