@@ -923,3 +923,20 @@ def test_random_shapes(seed):
     assert np.array_equal(blocks.cpu().numpy(), want)
     out, lse = _run(_bf16(q), kt, vt, table, seqs, blocks=blocks)
     _check(out, lse, q, kp, vp, table, seqs, PR.visible(seqs, table, page, n_pages, Hkv, want), D ** -0.5)
+
+
+@pytest.mark.parametrize("lq,lk,prefix,Hq,Hkv,D,page", [([1, 1, 1], [20, 90, 64], 70, 4, 2, 64, 16), ([5, 30], [7, 200], 128, 2, 1, 128, 64)])
+def test_the_first_sequence_of_a_group_is_the_shortest(lq, lk, prefix, Hq, Hkv, D, page):
+    """Its row of the table names all of the prefix's pages, though it holds fewer keys itself."""
+    _say("short first sequence", lq, lk, prefix, Hq, Hkv, D, page)
+    g = np.random.default_rng(sum(lk))
+    table, n_pages = _table(g, [max(lk)] + lk[1:], page)
+    for b, n in enumerate(lk):
+        full = prefix // page if n >= prefix else -(-n // page)
+        table[b, :full] = table[0, :full]
+    kp, vp, kt, vt = _pool(g, n_pages, page, Hkv, D)
+    q = AR.bf16(g.normal(0, 2, (sum(lq), Hq, D)))
+    seqs = _seqs(lq, lk)
+    out, lse = _run(_bf16(q), kt, vt, table, seqs, cu_group=_i32([0, len(lk)]), prefix_len=_i32([prefix]), max_prefix=prefix,
+                    max_kv=max(max(m - prefix, 0) for m in lk))
+    _check(out, lse, q, kp, vp, table, seqs, PR.visible(seqs, table, page, n_pages, Hkv), D ** -0.5)
