@@ -268,7 +268,8 @@ class PagedAttentionBlock(AttentionBlock):
 
     select (n_blocks, first, last): single-token plans attend to n_blocks pages of each sequence,
     its first and last ones and those whose keys' bounds promise the most, read for each sequence on its own, also
-    where sequences share them; None: to everything."""
+    where sequences share them; None: to everything.  (A plan that runs again begins the bounds of its pages anew:
+    tokens of later plans in its last page no longer count there.)"""
 
     def __init__(self, *args, page_size: int = 64, n_pages: int, select=None, **kw):
         self.page_size, self.n_pages, self.select = page_size, n_pages, select

@@ -1,6 +1,8 @@
 """The bookkeeping of PagedAttentionBlock on the CPU: stand-ins for the operators carry a token's number from x
 to its slot, and every call is checked for what its attention reads through the page table: token j of a
 sequence at position j, none missing, the same through the group's first sequence for what a group shares."""
+import random
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -373,3 +375,58 @@ def test_selecting_plans_have_no_groups(monkeypatch):
     m.fork(0, 1)
     m.step([2, 1])
     assert m.calls[-1][5] == ([0, 2], [96], 96)
+
+
+@pytest.mark.parametrize("seed", range(50))
+def test_random_walks(monkeypatch, seed):
+    """Plans, steps, cancels, forks, resets and second runs in any order: what a sequence reads is what it was fed, whatever the others
+    do, and every page is accounted for."""
+    r = random.Random(seed)
+    m = Model(monkeypatch, n_pages=r.choice([14, 24, 40]), max_len=160, select=r.choice([None, (4, 1, 2)]))
+    ran = []  # plans that have run, and how many tokens there were before
+    for _ in range(60):
+        do = r.choice(["step", "step", "decode", "cancel", "fork", "fork", "reset", "again", "again"])
+        held = [len(f) for f in m.fed]
+        new = [r.choice([0, 0, 0, 1, 5, 17, 40]) for _ in held]
+        new[r.randrange(4)] = r.choice([1, 30])
+        try:
+            if do == "step":
+                plan = m.b.plan(new)
+                m.step(new, plan)
+                ran.append((plan, held))
+            elif do == "decode":
+                who = [int(h > 0 and r.random() < 0.7) for h in held]
+                who[r.randrange(4)] = 1
+                plan = m.b.plan(who, max_kv=min(160, max(h + 1 for h, w in zip(held, who) if w) + r.randint(0, 20)))
+                for i in range(r.randint(1, min(5, plan.max_kv - plan.longest + 1))):
+                    if i:
+                        plan.advance()
+                    m.step(who, plan)
+            elif do == "cancel":
+                plan, other = m.b.plan(new), r.random() < 0.5
+                if other:
+                    m.b.plan([1] * 4).cancel()
+                plan.cancel()
+            elif do == "fork":
+                m.fork(r.randrange(4), r.randrange(4))
+            elif do == "reset":
+                b = r.randrange(4)
+                m.b.reset(b)
+                m.fed[b] = []
+            elif ran:
+                plan, at = r.choice(ran)
+                tokens = [r.randint(1, 200) for _ in range(sum(plan.new))]  # other ones in the same places
+                m.b.forward(torch.tensor(tokens).float()[:, None].expand(len(tokens), HIDDEN).bfloat16(), plan)
+                for s, n in enumerate(plan.new):
+                    m.fed[s][at[s]:at[s] + n], tokens = tokens[:n], tokens[n:]
+        except ValueError:
+            for plan in m.b._unrun:
+                assert len(plan) <= 1
+            for s in range(4):  # a plan that did not get to run
+                if m.b._unrun[s]:
+                    m.b.reset(s)
+                    m.fed[s] = []
+        m.check_pages()
+        for s, f in enumerate(m.fed):
+            assert m.b.held(s) == len(f)
+            assert m.read(m.b.table[s], len(f)) == [float(t) for t in f]
